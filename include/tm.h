@@ -489,6 +489,149 @@ int32_t tm_attn_kernel_choice(int64_t max_q, int64_t max_k, int32_t batch, int32
 tm_status tm_merge_head_shards(void* out, int64_t out_stride_t, const void* gathered, int64_t T, int32_t Hq,
                                int32_t d, int32_t world, int32_t h_cap, const int32_t* head_start, void* stream);
 
+/* ===========================================================================
+ * Serving over a paged K/V cache: rotary positions, norms of queries and
+ * keys, appending to the cache, reading it back, and attention for a batch
+ * that shares a prefix.  Forward passes only, as every entry of this library.
+ * ======================================================================== */
+
+/* Rotary positions.  Pair i (0 <= i < rot_dim / 2) of a head at position p is
+ * turned by the angle p * f_i:
+ *   y_a = m (x_a cos - x_b sin),  y_b = m (x_a sin + x_b cos),
+ * (a, b) = (i, i + rot_dim / 2) in the half layout, (2i, 2i + 1) in the
+ * interleaved one; dimensions from rot_dim on are copied.  turns[i] holds
+ * f_i / (2 pi) as a binary fraction of 64 bits, so that p * turns[i] modulo
+ * 2^64 is the angle in turns exactly to 2^-64 p: far positions lose nothing.
+ * Filled by tm_rope_init; a host structure, read during the call only. */
+typedef struct {
+  int32_t d, rot_dim, interleaved;
+  float mscale;
+  uint64_t turns[64];
+} tm_rope_freqs;
+
+typedef enum {
+  TM_ROPE_PLAIN = 0,   /* f_i = theta^(-2i / rot_dim) */
+  TM_ROPE_LINEAR = 1,  /* f_i / factor */
+  TM_ROPE_NTK = 2,     /* theta replaced by theta * factor^(rot_dim / (rot_dim - 2)) (rot_dim > 2) */
+  TM_ROPE_YARN = 3,    /* YaRN: f_i (1 - r_i) + f_i / factor * r_i, where r_i = clamp((i - lo) / max(hi - lo,
+                          0.001), 0, 1), lo = max(floor(c(fast)), 0), hi = min(ceil(c(slow)), rot_dim - 1),
+                          c(n) = rot_dim ln(original_max / (2 pi n)) / (2 ln theta); m = 0.1 ln(factor) + 1 */
+  TM_ROPE_BANDS = 4    /* f_i s_i + f_i / factor (1 - s_i), s_i = clamp((n_i - slow) / (fast - slow), 0, 1),
+                          n_i = original_max f_i / (2 pi): the turns pair i makes over the original length */
+} tm_rope_scaling;
+
+/* Fills *rope.  d in {64, 128}; rot_dim a multiple of 16, 16 <= rot_dim <= d;
+ * theta > 1; factor >= 1 and original_max > 0 where the scaling uses them;
+ * fast > slow > 0 for YARN (usual 32 and 1) and BANDS (usual 4 and 1).
+ * TM_ERR_INVALID_ARG otherwise.  Host-only. */
+tm_status tm_rope_init(tm_rope_freqs* rope, int32_t d, int32_t rot_dim, int32_t interleaved, double theta,
+                       int32_t scaling, double factor, double original_max, double fast, double slow);
+
+/* tm_rope -- rotates q (and k, may be NULL) by the rows' positions:
+ * row t has position positions[t] (device int32 [T]) + pos_offset, or
+ * t + pos_offset when positions is NULL.  q, k: fp16 [T, H, d] (codes / scales
+ * ignored), equal T, d = rope->d; q_out, k_out: same shapes, the same tensor
+ * (in place) or one that does not overlap it.  Computed in fp32 with one
+ * rounding at the end.  T = 0 is a no-op. */
+tm_status tm_rope(const tm_tensor* q, const tm_tensor* k, tm_tensor* q_out, tm_tensor* k_out,
+                  const tm_rope_freqs* rope, const int32_t* positions, int64_t pos_offset, void* stream);
+
+/* tm_qk_norm_rope -- per head x / sqrt(mean(x^2) + eps) * w, then tm_rope, in
+ * one pass with one rounding.  q_weight, k_weight: device fp16 [d], 16-byte
+ * aligned (k_weight ignored without k); rope NULL: the norm alone. */
+tm_status tm_qk_norm_rope(const tm_tensor* q, const tm_tensor* k, tm_tensor* q_out, tm_tensor* k_out,
+                          const void* q_weight, const void* k_weight, float eps, const tm_rope_freqs* rope,
+                          const int32_t* positions, int64_t pos_offset, void* stream);
+
+/* A pool of K/V pages.  Element c of head h of slot s of page p is at
+ * k[p * stride_page + s * stride_t + h * stride_h + c], v alike: fp16, or INT8
+ * codes when k_scales / v_scales are given (fp16, one per slot and head, at
+ * p * scale_stride_page + s * scale_stride_t + h * scale_stride_h; a value is
+ * code * scale).  page_size in {16, 32, 64, 128, 256}; d in {64, 128}; k and v
+ * 16-byte aligned, strides multiples of 16 bytes.  Pages of different tokens
+ * must not overlap. */
+typedef struct {
+  void *k, *v;
+  void *k_scales, *v_scales;   /* both or neither */
+  int32_t num_pages, page_size, H, d;
+  int64_t stride_page, stride_t, stride_h;
+  int64_t scale_stride_page, scale_stride_t, scale_stride_h;
+} tm_paged_kv;
+
+/* Block tables.  Own position j of sequence b is slot j % page_size of page
+ * table[b * table_stride + j / page_size] (device int32 [batch, table_cols]).
+ * Page numbers outside 0 .. num_pages-1, and positions past the table, are
+ * recorded in the device error word (TM_ERR_INVALID_ARG from
+ * tm_get_device_error) and neither read nor written; what depends on them is
+ * unspecified.  tm_block_table_check does the same test on host copies before
+ * anything is launched: TM_ERR_INVALID_ARG and the first bad (sequence,
+ * column) in bad[2] (may be NULL), TM_OK otherwise. */
+tm_status tm_block_table_check(const int32_t* table_host, int64_t table_stride, int32_t table_cols,
+                               const int32_t* kv_lens_host, int32_t batch, int32_t num_pages, int32_t page_size,
+                               int32_t* bad);
+
+/* ---------------------------------------------------------------------------
+ * tm_kv_append -- new tokens into the cache, rotated on the way.
+ * k, v: fp16 [T, H, d], rows packed by cu_seqlens (device int32 [batch + 1]),
+ * or T / batch rows for each sequence when cu_seqlens is NULL.  kv_lens[b]
+ * (device int32) is the length of sequence b AFTER the append: its new row i
+ * of n goes to own position j = kv_lens[b] - n + i and is rotated at position
+ * j + pos_offset (pos_offset: the length of a shared prefix).  Rows with j < 0
+ * (padding) and rows behind the last sequence are not appended.
+ *   k_weight / q_weight: fp16 [d] norm weights or NULL (no norm), eps as above;
+ *   rope: NULL for no rotation;
+ *   q, q_out: NULL, or the same tokens' queries, normed with q_weight and
+ *   rotated into q_out in the same launch (rows behind the last sequence are
+ *   left as they were).
+ * K is computed in fp32 and rounded once (fp16 pages) or quantised from fp32
+ * (INT8 pages); INT8: scale = fp16(amax / 127), code = clamp(rne(x / scale),
+ * -127, 127), all codes 0 where the scale is 0 (a row that holds a NaN or an
+ * infinity gets a scale that is one).  Two new rows with one slot leave either
+ * row, or a mix of both, there. */
+tm_status tm_kv_append(const tm_tensor* k, const tm_tensor* v, const tm_paged_kv* cache, const int32_t* table,
+                       int64_t table_stride, int32_t table_cols, const int32_t* kv_lens, const int32_t* cu_seqlens,
+                       int32_t batch, const tm_rope_freqs* rope, int64_t pos_offset, const tm_tensor* q,
+                       tm_tensor* q_out, const void* q_weight, const void* k_weight, float eps, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * tm_kv_gather -- cached rows back into contiguous fp16 tensors, as the
+ * prefill attention over separate key offsets reads them: row
+ * cu_seqlens_k[b] + j of k_out / v_out [T, H, d] is own position j of sequence
+ * b (INT8 pages: fp16(code * scale)).  Rows behind the last sequence, and rows
+ * whose page number is bad, are left as they were. */
+tm_status tm_kv_gather(const tm_paged_kv* cache, const int32_t* table, int64_t table_stride, int32_t table_cols,
+                       const int32_t* cu_seqlens_k, int32_t batch, tm_tensor* k_out, tm_tensor* v_out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * tm_attn_shared_prefix -- attention for a batch over a paged cache, with a
+ * prefix that all sequences share read and multiplied once for all of them.
+ *
+ * Query row i of sequence b (n_b rows; packed by cu_seqlens, or T / batch each
+ * when it is NULL) sees every prefix position 0 .. prefix_len-1 (pages
+ * prefix_pages, device int32, at least ceil(prefix_len / page_size); read
+ * by the whole batch) and own position j of its sequence iff j < kv_lens[b]
+ * and (not causal or j <= i + kv_lens[b] - n_b).  One softmax runs over both:
+ *   out = fp16( sum_j softmax_j(q . k_j / sqrt(d)) v_j )
+ * fp32 scores, statistics and sums; P rounded to fp16 for the P.V product.  A
+ * row that sees nothing is 0; rows behind the last sequence are left as they
+ * were.  Values at visible and causally hidden positions below kv_lens[b] must
+ * be finite; the rest of a page is never used.
+ *   prefix_len = 0: plain paged attention (prefix_pages may be NULL).
+ *   max_seqlen: bound on n_b (ignored without cu_seqlens); max_kv_len: bound
+ *   on kv_lens[b], at most table_cols * page_size, sizes the launch; a longer
+ *   sequence is recorded in the device error word and cut to it.
+ *   workspace: tm_attn_shared_prefix_workspace(...) bytes for the same
+ *   arguments, 256-byte aligned, owned by the caller, overwritten; calls that
+ *   may overlap on the GPU (other streams, graphs replayed side by side) need
+ *   one each. */
+int64_t tm_attn_shared_prefix_workspace(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t batch,
+                                        int32_t max_seqlen, int64_t prefix_len, int64_t max_kv_len);
+tm_status tm_attn_shared_prefix(const tm_tensor* q, const tm_paged_kv* cache, tm_tensor* out, const int32_t* table,
+                                int64_t table_stride, int32_t table_cols, const int32_t* kv_lens,
+                                const int32_t* cu_seqlens, int32_t batch, int32_t max_seqlen,
+                                const int32_t* prefix_pages, int64_t prefix_len, int64_t max_kv_len, int32_t causal,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* tm_status_string(tm_status s);
 

@@ -1,0 +1,709 @@
+// tm_attn_shared.cu -- attention of a batch over a paged cache behind a shared
+// prefix (tm_attn_shared_prefix): the split-key kernel for few rows, and the
+// join of partial results.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "tm_attn_shared.cuh"
+#include "tm_host.h"
+
+namespace tmk {
+
+SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t batch, int64_t max_seqlen,
+                       int64_t prefix_len, int64_t max_kv_len) {
+  SharedPlan p{};
+  p.group = Hq / Hkv;
+  const int64_t own_rows = (max_seqlen * p.group + 15) / 16, pre_rows = (T * p.group + 15) / 16;
+  const int64_t own_units = (max_kv_len + 127) / 128, pre_units = (prefix_len + 127) / 128;
+  const int64_t units = batch * own_rows * Hkv * own_units + pre_rows * Hkv * pre_units;
+  // two waves of one CTA per SM, every CTA with about the same keys
+  int64_t chunk = (units + 2 * kSmsB200 - 1) / (2 * kSmsB200);
+  const int64_t most = own_units > pre_units ? own_units : pre_units;
+  if (chunk < (most + 31) / 32) chunk = (most + 31) / 32;   // at most 32 splits of each
+  if (chunk < 1) chunk = 1;
+  p.own_rows = static_cast<int>(own_rows);
+  p.pre_rows = static_cast<int>(pre_rows);
+  p.own_chunk = p.pre_chunk = static_cast<int>(chunk * 128);
+  p.own_splits = static_cast<int>((own_units + chunk - 1) / chunk);
+  p.pre_splits = static_cast<int>((pre_units + chunk - 1) / chunk);
+  p.slots = p.own_splits + p.pre_splits;
+  const int64_t rows = T * Hq;
+  p.ml_bytes = (p.slots * rows * 8 + 255) / 256 * 256;
+  p.bytes = p.slots > 1 ? p.ml_bytes + p.slots * rows * d * 4 : 0;
+  if (p.bytes < 256) p.bytes = 256;
+  return p;
+}
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kStep = 32;     // keys of one warp step
+constexpr int kStages = 3;
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+// Two codes, as bytes code + 128 picked by `sel` from w, to a pair of fp16:
+// under the exponent byte 0x64 a byte b reads as 1024 + b, exactly.
+__device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sel) {
+  const uint32_t x = __byte_perm(w, 0x64646464u, sel);
+  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(1152.0f));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Bytes of one 32-key stage of K (V the same), and where the 16-byte piece c
+// of key row `row` lies in it: permuted so that the reads below (ldmatrix of
+// eight rows; for INT8, 16-byte reads of two rows' quarters for K and of four
+// even or odd rows for V) meet no bank twice.
+template <int D, bool INT8>
+struct Stage {
+  static constexpr int ROW = D * (INT8 ? 1 : 2);
+  static constexpr int BYTES = kStep * ROW;
+  static constexpr int PIECES = ROW / 16;
+  __device__ static __forceinline__ uint32_t at(int row, int c, bool is_v) {
+    if (!INT8) return row * ROW + ((c ^ (row & 7)) << 4);
+    if (D == 128) return row * ROW + ((c ^ (is_v ? ((row >> 1) & 3) << 1 : (row & 1) << 2)) << 4);
+    const int line = row >> 1, i = ((row & 1) << 2) | c;
+    return line * 128 + ((i ^ ((line & 3) << 1)) << 4);
+  }
+};
+
+template <int D, bool INT8>
+constexpr int split_smem() {
+  return kWarps * kStages * (2 * Stage<D, INT8>::BYTES + (INT8 ? 2 * kStep * 4 : 0)) + kWarps * 16 * 8;
+}
+
+// Attention of up to 16 packed rows over one range of keys.
+//
+// Decoding reads far more than it computes (a key's 2 d values serve g rows),
+// so this is built around the copies: each of the four warps owns every fourth
+// 32-key step and its own three-stage ring of cp.async copies, with no
+// barrier between warps until the join at the end.  At d = 128 in fp16 a stage
+// is 16 KB, so 128 KB per SM are in flight while a third of the ring is
+// computed on.  Rows of a step past the range's end are filled with zeros
+// and never read from memory.  The products run on mma.sync m16n8k16: 16 rows
+// hold a whole group of query heads, where a 128-row tensor-memory tile would
+// be nearly empty.
+//
+// INT8: K and V stay codes in shared memory and become fp16 in registers
+// (exactly); a key's K scale multiplies its scores and its V scale its P,
+// which costs two roundings fewer than scaling the codes.  The code layouts
+// follow the fragments: the order of d within the QK^T sum is free, so a
+// lane's 16 consecutive codes serve four MMAs; the order of output columns is
+// free too, so a lane's n index stands for d / 8 consecutive dimensions.
+template <int D, bool INT8>
+__global__ void __launch_bounds__(kWarps * 32) split_kernel(const __grid_constant__ SharedArgs a, DevErr err) {
+  using S = Stage<D, INT8>;
+  constexpr int NT = D / 8, KS = D / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = lane & 3, r8 = lane >> 2;
+  const SharedPlan& p = a.plan;
+  const int H = a.pool.H, g = p.group, Hq = H * g;
+
+  // ---- which rows and keys
+  int64_t item = blockIdx.x;
+  const int kvh = static_cast<int>(item % H);
+  item /= H;
+  const int64_t pre_items = static_cast<int64_t>(p.pre_splits) * p.pre_rows;
+  const bool prefix = item < pre_items;
+  int b = 0, slot;
+  int64_t row0, start = 0, nrows, k0, k1, hidden = 0;   // hidden: own keys that row 0's token does not see
+  int64_t lk = 0;
+  if (prefix) {
+    row0 = (item % p.pre_rows) * 16;
+    slot = static_cast<int>(item / p.pre_rows);
+    nrows = a.T * g;
+    k0 = static_cast<int64_t>(slot) * p.pre_chunk;
+    k1 = k0 + p.pre_chunk < a.prefix_len ? k0 + p.pre_chunk : a.prefix_len;
+    lk = a.prefix_len;
+  } else {
+    item -= pre_items;
+    const int64_t per = static_cast<int64_t>(a.batch) * p.own_rows;
+    const int split = static_cast<int>(item / per);
+    item %= per;
+    b = static_cast<int>(item / p.own_rows);
+    row0 = (item % p.own_rows) * 16;
+    slot = p.pre_splits + split;
+    int64_t n;
+    seq_rows(a, b, start, n);
+    nrows = n * g;
+    const bool outside = start < 0 || start + n > a.T || nrows > static_cast<int64_t>(p.own_rows) * 16;
+    if (outside && threadIdx.x == 0) dev_error(err, TM_DEVERR_SEQLEN);   // offsets that the launch was not sized for
+    if (outside || row0 >= nrows) return;
+    lk = __ldg(a.kv_lens + b);
+    if (lk > a.max_kv) {
+      if (threadIdx.x == 0) dev_error(err, TM_DEVERR_SEQLEN);
+      lk = a.max_kv;
+    }
+    if (lk < 0) lk = 0;
+    const int64_t last = (row0 + 16 < nrows ? row0 + 16 : nrows) - 1;
+    const int64_t seen = a.causal ? last / g + lk - n + 1 : lk;   // keys the block's last row sees
+    k0 = static_cast<int64_t>(split) * p.own_chunk;
+    k1 = k0 + p.own_chunk < lk ? k0 + p.own_chunk : lk;
+    if (k1 > seen) k1 = seen;
+    hidden = a.causal ? lk - n + 1 : lk;    // token i of the sequence sees keys below hidden + i (causal)
+  }
+  const int rows = static_cast<int>(nrows - row0 < 16 ? nrows - row0 : 16);
+  const int64_t total = static_cast<int64_t>(a.T) * Hq;
+  const bool direct = p.slots == 1;
+
+  // (token, query head) of packed row r of this block
+  auto token_of = [&](int r) { return start + (row0 + r) / g; };
+  auto head_of = [&](int r) { return kvh * g + static_cast<int>((row0 + r) % g); };
+
+  if (k0 >= k1) {     // nothing visible here
+    if (!direct) {
+      if (threadIdx.x < rows)
+        a.ml[slot * total + token_of(threadIdx.x) * Hq + head_of(threadIdx.x)] = make_float2(-INFINITY, 0.f);
+    } else {
+      for (int i = threadIdx.x; i < rows * (D / 8); i += kWarps * 32) {
+        const int r = i / (D / 8);
+        if (token_of(r) < rows_in_use(a))
+          *reinterpret_cast<uint4*>(a.out + token_of(r) * a.o_t + head_of(r) * a.o_h + (i % (D / 8)) * 8) =
+              make_uint4(0, 0, 0, 0);
+      }
+    }
+    return;
+  }
+
+  // ---- this lane's rows r8 and r8 + 8: limits and Q fragments
+  int64_t lim[2];
+  uint32_t qf[KS][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = r8 + 8 * i;
+    const bool real = r < rows;
+    lim[i] = lk;
+    if (!prefix && a.causal && real) {
+      const int64_t l = hidden + (row0 + r) / g;
+      lim[i] = l < lk ? l : lk;
+    }
+    const __half* q = real ? a.q + token_of(r) * a.q_t + head_of(r) * a.q_h : a.q;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      if (INT8) {
+        // k-step s: codes (D / 4) * (s / 4 ...): lane's 16-byte piece s / 4 (d = 128: at 64 (s / 4) + 16 quad), word s % 4
+        const int at = (s >> 2) * 64 + quad * 16 + (s & 3) * 4;
+        const uint2 v = real ? *reinterpret_cast<const uint2*>(q + at) : make_uint2(0, 0);
+        qf[s][i] = v.x;
+        qf[s][2 + i] = v.y;
+      } else {
+        qf[s][i] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * quad) : 0u;
+        qf[s][2 + i] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 8 + 2 * quad) : 0u;
+      }
+    }
+  }
+  // steps that end at or below this key need no mask
+  int64_t open = k1;
+  if (!prefix && a.causal) {
+    const int64_t l = hidden + row0 / g;
+    if (l < open) open = l;
+  }
+
+  uint8_t* ring = smem + warp * kStages * 2 * S::BYTES;
+  const uint32_t ring_s = smem_u32(ring);
+  float* scales = reinterpret_cast<float*>(smem + kWarps * kStages * 2 * S::BYTES) + warp * kStages * 2 * kStep;
+  float2* ml_s = reinterpret_cast<float2*>(smem + kWarps * kStages * (2 * S::BYTES + (INT8 ? 2 * kStep * 4 : 0)));
+
+  const uint8_t* kbase = a.pool.k + kvh * a.pool.stride_h;
+  const uint8_t* vbase = a.pool.v + kvh * a.pool.stride_h;
+  const int64_t first = k0 + warp * kStep;
+  const int steps = first < k1 ? static_cast<int>((k1 - first + kWarps * kStep - 1) / (kWarps * kStep)) : 0;
+  const int shift = a.pool.page_shift;
+
+  // page of this lane's key of step i, -1 where nothing is to be read
+  auto page_at = [&](int i) -> int32_t {
+    const int64_t key = first + static_cast<int64_t>(i) * kWarps * kStep + lane;
+    if (i >= steps || key >= k1) return -1;
+    int32_t page;
+    if (prefix) {
+      page = __ldg(a.prefix_pages + (key >> shift));
+      if (!page_ok(page, a.pool.num_pages)) page = -1;
+    } else {
+      page = page_of(a.pt, b, key);
+    }
+    if (page < 0) dev_error(err, TM_DEVERR_SEQLEN);
+    return page;
+  };
+  float pend_k = 0.f, pend_v = 0.f;
+  // copies of step i into its stage; the scales follow one call later
+  auto issue = [&](int i, int32_t page) {
+    if (INT8 && i > 0) {
+      const int st = (i - 1) % kStages;
+      scales[st * 2 * kStep + lane] = pend_k;
+      scales[st * 2 * kStep + kStep + lane] = pend_v;
+    }
+    if (i < steps) {
+      const int64_t key = first + static_cast<int64_t>(i) * kWarps * kStep + lane;
+      const int64_t s = key & ((1 << shift) - 1);
+      const int64_t off = page >= 0 ? page * a.pool.stride_page + s * a.pool.stride_t : -1;
+      if (INT8) {
+        const int64_t so = page * a.pool.sstride_page + s * a.pool.sstride_t + kvh * a.pool.sstride_h;
+        pend_k = page >= 0 ? __half2float(a.pool.ks[so]) : 0.f;
+        pend_v = page >= 0 ? __half2float(a.pool.vs[so]) : 0.f;
+      }
+      const uint32_t dst = ring_s + (i % kStages) * 2 * S::BYTES;
+      constexpr int RPI = 32 / S::PIECES;
+      const int c = lane % S::PIECES;
+#pragma unroll
+      for (int n = 0; n < kStep / RPI; ++n) {
+        const int row = n * RPI + lane / S::PIECES;
+        const int64_t o = __shfl_sync(0xffffffffu, off, row);
+        const bool real = o >= 0;
+        cp16(dst + S::at(row, c, false), kbase + (real ? o + c * 16 : 0), real);
+        cp16(dst + S::BYTES + S::at(row, c, true), vbase + (real ? o + c * 16 : 0), real);
+      }
+    }
+    cp_commit();
+  };
+
+  float o[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+  int32_t page = page_at(0), page1 = page_at(1);
+  issue(0, page);
+  page = page_at(2);
+  issue(1, page1);
+
+  for (int i = 0; i < steps; ++i) {
+    cp_wait<1>();
+    __syncwarp();
+    issue(i + 2, page);      // into the stage that step i - 1 used
+    page = page_at(i + 3);
+    const uint32_t ks_s = ring_s + (i % kStages) * 2 * S::BYTES;
+    const uint32_t vs_s = ks_s + S::BYTES;
+    const float* sc = scales + (i % kStages) * 2 * kStep;
+    const int64_t key0 = first + static_cast<int64_t>(i) * kWarps * kStep;
+
+    float s[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+    if (!INT8) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ks += 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t bfr[4];
+          ldsm4(ks_s + S::at(8 * j + (lane & 7), 2 * ks + (lane >> 3), false), bfr);
+          mma16816(s[j], qf[ks], bfr[0], bfr[1]);
+          mma16816(s[j], qf[ks + 1], bfr[2], bfr[3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < KS / 4; ++c) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 v = lds128(ks_s + S::at(8 * j + r8, 4 * c + quad, false));
+          const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mma16816(s[j], qf[4 * c + e], codes2(w[e], 0x4140u), codes2(w[e], 0x4342u));
+        }
+      }
+    }
+
+    // scores in powers of two; hidden keys to -inf by selection, whatever they hold
+    float x[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float k0s = a.scale_log2, k1s = a.scale_log2;
+      if (INT8) {
+        const float2 f = *reinterpret_cast<const float2*>(sc + 8 * j + 2 * quad);
+        k0s *= f.x;
+        k1s *= f.y;
+      }
+      x[j][0] = s[j][0] * k0s;
+      x[j][1] = s[j][1] * k1s;
+      x[j][2] = s[j][2] * k0s;
+      x[j][3] = s[j][3] * k1s;
+    }
+    if (key0 + kStep > open) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t key = key0 + 8 * j + 2 * quad + (e & 1);
+          if (key >= k1 || key >= lim[e >> 1]) x[j][e] = -INFINITY;
+        }
+      }
+    }
+    float scale[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(x[j][2 * h], x[j][2 * h + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[h], mx);
+      const float use = mn == -INFINITY ? 0.f : mn;
+      scale[h] = ex2_approx(m[h] - use);
+      m[h] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float pr = ex2_approx(x[j][2 * h + e] - use + kPOffset);
+          x[j][2 * h + e] = pr;
+          sum += pr;
+        }
+      }
+      l[h] = l[h] * scale[h] + sum;
+    }
+    if (__any_sync(0xffffffffu, scale[0] != 1.f || scale[1] != 1.f)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        o[n][0] *= scale[0];
+        o[n][1] *= scale[0];
+        o[n][2] *= scale[1];
+        o[n][3] *= scale[1];
+      }
+    }
+#pragma unroll
+    for (int k2 = 0; k2 < 2; ++k2) {
+      if (INT8) {
+#pragma unroll
+        for (int j = 2 * k2; j < 2 * k2 + 2; ++j) {
+          const float2 f = *reinterpret_cast<const float2*>(sc + kStep + 8 * j + 2 * quad);
+          x[j][0] *= f.x;
+          x[j][1] *= f.y;
+          x[j][2] *= f.x;
+          x[j][3] *= f.y;
+        }
+      }
+      const uint32_t pf[4] = {pack_half2(x[2 * k2][0], x[2 * k2][1]), pack_half2(x[2 * k2][2], x[2 * k2][3]),
+                              pack_half2(x[2 * k2 + 1][0], x[2 * k2 + 1][1]),
+                              pack_half2(x[2 * k2 + 1][2], x[2 * k2 + 1][3])};
+      if (!INT8) {
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          uint32_t bfr[4];
+          ldsm4t(vs_s + S::at(16 * k2 + ((lane >> 3) & 1) * 8 + (lane & 7), n + (lane >> 4), true), bfr);
+          mma16816(o[n], pf, bfr[0], bfr[1]);
+          mma16816(o[n + 1], pf, bfr[2], bfr[3]);
+        }
+      } else {
+        // keys 2 quad, 2 quad + 1, 2 quad + 8, 2 quad + 9 of the 16; this lane's n index r8 stands for
+        // dimensions r8 * (D / 8) + n of n-tile n
+        uint32_t w[4][D / 32];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = 16 * k2 + 2 * quad + (e & 1) + 8 * (e >> 1);
+          if (D == 128) {
+            const uint4 v = lds128(vs_s + S::at(row, r8, true));
+            w[e][0] = v.x ^ 0x80808080u;
+            w[e][1] = v.y ^ 0x80808080u;
+            w[e][D / 32 - 2] = v.z ^ 0x80808080u;
+            w[e][D / 32 - 1] = v.w ^ 0x80808080u;
+          } else {
+            const uint2 v = lds64(vs_s + S::at(row, r8 >> 1, true) + (r8 & 1) * 8);
+            w[e][0] = v.x ^ 0x80808080u;
+            w[e][1] = v.y ^ 0x80808080u;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+#pragma unroll
+          for (int hlf = 0; hlf < 2; ++hlf) {
+            const uint32_t lo = __byte_perm(w[0][q], w[1][q], hlf ? 0x7362u : 0x5140u);
+            const uint32_t hi = __byte_perm(w[2][q], w[3][q], hlf ? 0x7362u : 0x5140u);
+            mma16816(o[4 * q + 2 * hlf], pf, codes2(lo, 0x4140u), codes2(hi, 0x4140u));
+            mma16816(o[4 * q + 2 * hlf + 1], pf, codes2(lo, 0x4342u), codes2(hi, 0x4342u));
+          }
+        }
+      }
+    }
+  }
+  cp_wait<0>();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+  }
+
+  // ---- join the four warps, in fragment order: register e of n-tile n of lane
+  if (quad == 0) {
+    ml_s[warp * 16 + r8] = make_float2(m[0], l[0]);
+    ml_s[warp * 16 + r8 + 8] = make_float2(m[1], l[1]);
+  }
+  __syncwarp();
+  float* os = reinterpret_cast<float*>(ring);    // this warp's ring, no longer read
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    *reinterpret_cast<float4*>(os + (n * 32 + lane) * 4) = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
+  __syncthreads();
+  float wgt[2][kWarps], M[2], L[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    M[h] = -INFINITY;
+    L[h] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M[h] = fmaxf(M[h], ml_s[w * 16 + r8 + 8 * h].x);
+    const float use = M[h] == -INFINITY ? 0.f : M[h];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 f = ml_s[w * 16 + r8 + 8 * h];
+      wgt[h][w] = ex2_approx(f.x - use);
+      L[h] += wgt[h][w] * f.y;
+    }
+    if (direct) {
+      const float inv = L[h] > 0.f ? 1.f / L[h] : (L[h] == 0.f ? 0.f : L[h]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) wgt[h][w] *= inv;
+    }
+  }
+  constexpr int NW = NT / kWarps;    // n-tiles per warp
+  float acc[NW][4];
+#pragma unroll
+  for (int n = 0; n < NW; ++n) {
+    acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float* src = reinterpret_cast<const float*>(smem + w * kStages * 2 * S::BYTES);
+      const float4 f = *reinterpret_cast<const float4*>(src + ((warp * NW + n) * 32 + lane) * 4);
+      acc[n][0] += wgt[0][w] * f.x;
+      acc[n][1] += wgt[0][w] * f.y;
+      acc[n][2] += wgt[1][w] * f.z;
+      acc[n][3] += wgt[1][w] * f.w;
+    }
+  }
+  const int64_t used = direct ? rows_in_use(a) : 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = r8 + 8 * h;
+    if (r >= rows) continue;
+    const int64_t t = token_of(r);
+    const int64_t idx = slot * total + t * Hq + head_of(r);
+    if (!direct && warp == 0 && quad == 0) a.ml[idx] = make_float2(M[h], L[h]);
+    if (direct && t >= used) continue;
+    __half* oh = direct ? a.out + t * a.o_t + head_of(r) * a.o_h : nullptr;
+    float* of = direct ? nullptr : a.o + idx * D;
+    if (INT8) {
+      // n-tiles warp * NW ..: consecutive dimensions for each of the lane's two columns
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int at = (2 * quad + e) * (D / 8) + warp * NW;
+#pragma unroll
+        for (int n = 0; n < NW; n += 2) {
+          if (direct)
+            *reinterpret_cast<uint32_t*>(oh + at + n) = pack_half2(acc[n][2 * h + e], acc[n + 1][2 * h + e]);
+          else
+            *reinterpret_cast<float2*>(of + at + n) = make_float2(acc[n][2 * h + e], acc[n + 1][2 * h + e]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NW; ++n) {
+        const int at = (warp * NW + n) * 8 + 2 * quad;
+        if (direct)
+          *reinterpret_cast<uint32_t*>(oh + at) = pack_half2(acc[n][2 * h], acc[n][2 * h + 1]);
+        else
+          *reinterpret_cast<float2*>(of + at) = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+      }
+    }
+  }
+}
+
+// Joins a row's splits: one warp per (token, query head), the slots' (m, l)
+// across the lanes, then the O rows that carry weight.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ SharedArgs a) {
+  const int Hq = a.pool.H * a.plan.group;
+  const int64_t total = a.T * Hq;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= total) return;
+  const int64_t t = row / Hq;
+  if (t >= rows_in_use(a) || (a.cu != nullptr && t < __ldg(a.cu))) return;
+  constexpr int V = D / 32;
+  float acc[V] = {}, M = -INFINITY, L = 0.f;
+  for (int s0 = 0; s0 < a.plan.slots; s0 += 32) {
+    const int n = a.plan.slots - s0 < 32 ? a.plan.slots - s0 : 32;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < n) ml = a.ml[(s0 + lane) * total + row];
+    float mx = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float mn = fmaxf(M, mx);
+    const float use = mn == -INFINITY ? 0.f : mn;
+    const float keep = ex2_approx(M - use);
+    const float w = ml.y == 0.f ? 0.f : ex2_approx(ml.x - use);
+    float sum = w * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    L = L * keep + sum;
+    M = mn;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] *= keep;
+    unsigned live = __ballot_sync(0xffffffffu, w != 0.f);   // NaN counts as live
+    while (live) {
+      const int s = __ffs(live) - 1;
+      live &= live - 1;
+      const float ws = __shfl_sync(0xffffffffu, w, s);
+      const float* src = a.o + ((s0 + s) * total + row) * D + lane * V;
+      if (V == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        acc[0] += ws * f.x;
+        acc[1] += ws * f.y;
+        acc[V - 2] += ws * f.z;
+        acc[V - 1] += ws * f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        acc[0] += ws * f.x;
+        acc[1] += ws * f.y;
+      }
+    }
+  }
+  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+  __half* dst = a.out + t * a.o_t + (row - t * Hq) * a.o_h + lane * V;
+  if (V == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_half2(acc[0] * inv, acc[1] * inv),
+                                                pack_half2(acc[V - 2] * inv, acc[V - 1] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_half2(acc[0] * inv, acc[1] * inv);
+}
+
+template <int D, bool INT8>
+tm_status launch(const SharedArgs& a, DevErr err, cudaStream_t stream) {
+  constexpr int smem = split_smem<D, INT8>();
+  static std::atomic<uint64_t> prepared{0};     // devices whose kernel has its shared memory
+  int dev = 0;
+  tm_status st = check_cuda(cudaGetDevice(&dev));
+  if (st != TM_OK) return st;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(prepared.load(std::memory_order_relaxed) & bit)) {
+    st = check_cuda(cudaFuncSetAttribute(split_kernel<D, INT8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (st != TM_OK) return st;
+    prepared.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const SharedPlan& p = a.plan;
+  const int64_t items = (static_cast<int64_t>(p.pre_splits) * p.pre_rows +
+                         static_cast<int64_t>(p.own_splits) * a.batch * p.own_rows) * a.pool.H;
+  if (items > 0x7fffffff) return TM_ERR_UNSUPPORTED;
+  if (items > 0) {
+    split_kernel<D, INT8><<<static_cast<unsigned>(items), kWarps * 32, smem, stream>>>(a, err);
+    st = check_cuda(cudaGetLastError());
+    if (st != TM_OK) return st;
+  }
+  if (p.slots == 1) return TM_OK;
+  const int64_t rows = a.T * a.pool.H * p.group;
+  const int64_t blocks = (rows + 7) / 8;
+  if (blocks > 0x7fffffff) return TM_ERR_UNSUPPORTED;
+  join_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
+  return check_cuda(cudaGetLastError());
+}
+
+bool plan_args_ok(int64_t T, int32_t Hq, int32_t Hkv, int32_t batch, int64_t max_seqlen, int64_t prefix_len,
+                  int64_t max_kv_len) {
+  return T >= 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && batch > 0 && max_seqlen >= 0 && prefix_len >= 0 &&
+         max_kv_len >= 0 && prefix_len <= (1ll << 30) && max_kv_len <= (1ll << 30) && T <= (1ll << 24) &&
+         static_cast<int64_t>(Hq) * T <= (1ll << 30) && Hq <= 65536;
+}
+
+}  // namespace
+}  // namespace tmk
+
+extern "C" int64_t tm_attn_shared_prefix_workspace(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t batch,
+                                                   int32_t max_seqlen, int64_t prefix_len, int64_t max_kv_len) {
+  if (!tmk::plan_args_ok(T, Hq, Hkv, batch, max_seqlen, prefix_len, max_kv_len) || (d != 64 && d != 128)) return -1;
+  return tmk::shared_plan(T, Hq, Hkv, d, batch, max_seqlen, prefix_len, max_kv_len).bytes;
+}
+
+extern "C" tm_status tm_attn_shared_prefix(const tm_tensor* q, const tm_paged_kv* cache, tm_tensor* out,
+                                           const int32_t* table, int64_t table_stride, int32_t table_cols,
+                                           const int32_t* kv_lens, const int32_t* cu_seqlens, int32_t batch,
+                                           int32_t max_seqlen, const int32_t* prefix_pages, int64_t prefix_len,
+                                           int64_t max_kv_len, int32_t causal, void* workspace,
+                                           int64_t workspace_bytes, void* stream) {
+  using namespace tmk;
+  SharedArgs a{};
+  bool int8 = false;
+  tm_status st = paged_pool(cache, &a.pool, &int8);
+  if (st != TM_OK) return st;
+  st = page_table(a.pool, table, table_stride, table_cols, &a.pt);
+  if (st != TM_OK) return st;
+  if (q == nullptr || out == nullptr || kv_lens == nullptr || batch <= 0) return TM_ERR_INVALID_ARG;
+  const int64_t T = q->T, d = cache->d;
+  if (T < 0 || !thd_ok(q, T, q->H, d) || !thd_out_ok(out, T, q->H, d)) return TM_ERR_INVALID_ARG;
+  if (cu_seqlens == nullptr) {
+    if (T % batch != 0) return TM_ERR_INVALID_ARG;
+    if (T / batch > 0x7fffffff) return TM_ERR_UNSUPPORTED;
+    max_seqlen = static_cast<int32_t>(T / batch);
+  }
+  if (q->H > 65536 || !plan_args_ok(T, static_cast<int32_t>(q->H), cache->H, batch, max_seqlen, prefix_len, max_kv_len))
+    return TM_ERR_INVALID_ARG;
+  if (prefix_len > 0 && prefix_pages == nullptr) return TM_ERR_INVALID_ARG;
+  if (max_kv_len > static_cast<int64_t>(table_cols) * cache->page_size) return TM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(kv_lens) | reinterpret_cast<uintptr_t>(cu_seqlens) |
+       reinterpret_cast<uintptr_t>(prefix_pages)) & 3u)
+    return TM_ERR_INVALID_ARG;
+  a.plan = shared_plan(T, static_cast<int32_t>(q->H), cache->H, cache->d, batch, max_seqlen, prefix_len, max_kv_len);
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < a.plan.bytes)
+    return TM_ERR_INVALID_ARG;
+  if (T == 0) return TM_OK;
+  a.q = static_cast<const __half*>(q->data);
+  a.q_t = q->stride_t;
+  a.q_h = q->stride_h;
+  a.out = static_cast<__half*>(out->data);
+  a.o_t = out->stride_t;
+  a.o_h = out->stride_h;
+  a.kv_lens = kv_lens;
+  a.cu = cu_seqlens;
+  a.prefix_pages = prefix_pages;
+  a.T = T;
+  a.per_seq = T / batch;
+  a.prefix_len = prefix_len;
+  a.max_kv = max_kv_len;
+  a.batch = batch;
+  a.causal = causal != 0;
+  a.ml = static_cast<float2*>(workspace);
+  a.o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a.plan.ml_bytes);
+  a.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(d)));
+  const DevErr err{device_error_word()};
+  if (err.word == nullptr) return cuda_fail(static_cast<int>(cudaErrorInvalidSymbol));
+  cudaStream_t s = as_stream(stream);
+  if (d == 128) return int8 ? launch<128, true>(a, err, s) : launch<128, false>(a, err, s);
+  return int8 ? launch<64, true>(a, err, s) : launch<64, false>(a, err, s);
+}

@@ -33,6 +33,18 @@ class TmError(RuntimeError):
                          + (f", cuda {_lib().tm_last_cuda_error()})" if status == TM_ERR_CUDA else ")"))
 
 
+class TmRopeFreqs(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("mscale", ctypes.c_float), ("turns", ctypes.c_uint64 * 64)]
+
+
+class TmPagedKv(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scales", "v_scales")]
+                + [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "H", "d")]
+                + [(n, ctypes.c_int64) for n in ("stride_page", "stride_t", "stride_h", "scale_stride_page",
+                                                 "scale_stride_t", "scale_stride_h")])
+
+
 class TmTensor(ctypes.Structure):
     _fields_ = [
         ("data", ctypes.c_void_p),
@@ -56,6 +68,7 @@ def _lib():
         lib = ctypes.CDLL(LIB_PATH)
         P, I32, I64, U64, D = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_double
         TP = ctypes.POINTER(TmTensor)
+        RP, KP, F = ctypes.POINTER(TmRopeFreqs), ctypes.POINTER(TmPagedKv), ctypes.c_float
         sig = {
             "tm_quantize_qk": (I32, [TP, TP, P, P, P, P, P, I32, I32, I32, I32, P]),
             "tm_mask_words": (I32, [I64, I32, I32]),
@@ -92,6 +105,14 @@ def _lib():
             "tm_set_attn_kernel": (I32, [I32]),
             "tm_attn_kernel_choice": (I32, [I64, I64, I32, I32, I32, I32, I32, I32]),
             "tm_quantize_qk_fp8": (I32, [TP, TP, P, P, P, P, P, I32, I32, I32, I32, P]),
+            "tm_rope_init": (I32, [RP, I32, I32, I32, D, I32, D, D, D, D]),
+            "tm_rope": (I32, [TP, TP, TP, TP, RP, P, I64, P]),
+            "tm_qk_norm_rope": (I32, [TP, TP, TP, TP, P, P, F, RP, P, I64, P]),
+            "tm_block_table_check": (I32, [P, I64, I32, P, I32, I32, I32, P]),
+            "tm_kv_append": (I32, [TP, TP, KP, P, I64, I32, P, P, I32, RP, I64, TP, TP, P, P, F, P]),
+            "tm_kv_gather": (I32, [KP, P, I64, I32, P, I32, TP, TP, P]),
+            "tm_attn_shared_prefix_workspace": (I64, [I64, I32, I32, I32, I32, I32, I64, I64]),
+            "tm_attn_shared_prefix": (I32, [TP, KP, TP, P, I64, I32, P, P, I32, I32, P, I64, I64, I32, P, I64, P]),
             "tm_attn_fwd_fp8": (I32, [TP, TP, TP, TP, P, I32, I32, P, P, I64, P, P, P, P, I32, I32, P]),
         }
         for name, (res, args) in sig.items():
@@ -646,6 +667,297 @@ def merge_head_shards(out, gathered, head_start):
     st = _lib().tm_merge_head_shards(_ptr(out), int(out.stride(0)), _ptr(gathered), int(T), int(out.shape[1]),
                                      int(d), int(world), int(h_cap), hs.ctypes.data, _stream())
     _check(st, "tm_merge_head_shards")
+    return out
+
+
+# ------------------------------------------------- serving over a paged cache
+ROPE_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+
+class Rope:
+    """Rotary positions of heads of d values (tm_rope_init): the first rot_dim
+    of them turned (default all; a multiple of 16), in pairs (i, i +
+    rot_dim / 2), or (2i, 2i + 1) when interleaved.  scaling for contexts
+    longer than original_max: None, "linear", "ntk", "yarn" or "bands" (see
+    tm_rope_scaling in include/tm.h), by factor; fast / slow default to 32 / 1
+    for "yarn" and 4 / 1 for "bands".  Host object; keep one for each model."""
+
+    def __init__(self, d, rot_dim=None, *, theta=10000.0, interleaved=False, scaling=None, factor=1.0,
+                 original_max=4096, fast=None, slow=None):
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling: one of {tuple(ROPE_SCALINGS)} expected")
+        self.d, self.rot_dim = int(d), int(d if rot_dim is None else rot_dim)
+        self.struct = TmRopeFreqs()
+        fast = (4.0 if scaling == "bands" else 32.0) if fast is None else fast
+        _check(_lib().tm_rope_init(ctypes.byref(self.struct), self.d, self.rot_dim, int(bool(interleaved)), float(theta),
+                                   ROPE_SCALINGS[scaling], float(factor), float(original_max), float(fast),
+                                   float(1.0 if slow is None else slow)), "tm_rope_init")
+        self._ref = ctypes.byref(self.struct)
+
+
+class PagedKV:
+    """A pool of K/V pages (tm_paged_kv): k, v [num_pages, page_size, Hkv, d],
+    fp16, or INT8 codes with fp16 scales [num_pages, page_size, Hkv] for each
+    slot and head.  Any strides with the innermost dimension contiguous (heads
+    before slots, say), the same for K and V.  Wraps the caller's tensors and
+    keeps them alive; page_size in {16, 32, 64, 128, 256}, d in {64, 128}."""
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or v.dtype != k.dtype:
+            raise ValueError("k, v: [num_pages, page_size, Hkv, d] of one shape, type and layout expected")
+        if k.stride(3) != 1:
+            raise ValueError("innermost dimension must be contiguous")
+        self.int8 = k.dtype == torch.int8
+        if self.int8 != (k_scales is not None) or self.int8 != (v_scales is not None):
+            raise ValueError("INT8 pages come with k_scales and v_scales, fp16 pages without")
+        if not self.int8 and k.dtype != torch.float16:
+            raise ValueError("fp16 or int8 pages expected")
+        for t, n in ((k, "k"), (v, "v"), (k_scales, "k_scales"), (v_scales, "v_scales")):
+            _cuda(t, n)
+            if t is not None and t.device != k.device:
+                raise ValueError(f"{n}: all of a cache lies on one device")
+        st = (0, 0, 0)
+        if self.int8:
+            for t in (k_scales, v_scales):
+                if t.dtype != torch.float16 or t.shape != k.shape[:3] or t.stride() != k_scales.stride():
+                    raise ValueError("k_scales, v_scales: fp16 [num_pages, page_size, Hkv] of one layout expected")
+            st = k_scales.stride()
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.device = k.device
+        self.num_pages, self.page_size, self.H, self.d = k.shape
+        if self.d not in (64, 128) or self.page_size not in (16, 32, 64, 128, 256):
+            raise ValueError("page_size in {16, 32, 64, 128, 256} and d in {64, 128} expected")
+        if min(k.stride()[:3]) <= 0 or (self.int8 and min(st) <= 0):
+            raise ValueError("pages, slots and heads must not share memory")
+        self.struct = TmPagedKv(k.data_ptr(), v.data_ptr(), k_scales.data_ptr() if self.int8 else None,
+                                v_scales.data_ptr() if self.int8 else None, *k.shape, *k.stride()[:3], *st)
+        self._ref = ctypes.byref(self.struct)
+
+
+def _call(dev, name, *args):
+    """A library entry on the current stream of dev, whichever device is current."""
+    fn = getattr(_lib(), name)
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream())
+    else:
+        st = fn(*args, _stream())
+    if st != TM_OK:
+        raise TmError(st, name)
+
+
+def _thd(x, name, dev, T=None, H=None, d=None):
+    """tm_tensor of an fp16 [T, H, d] operand on dev."""
+    if x.dtype != torch.float16 or x.dim() != 3:
+        raise ValueError(f"{name}: fp16 [T, H, d] expected")
+    _cuda(x, name)
+    if x.device != dev:
+        raise ValueError(f"{name}: on {x.device}, the call is on {dev}")
+    a, b, c = x.shape
+    st, sh, sd = x.stride()
+    if sd != 1 and c != 1:
+        raise ValueError(f"{name}: innermost dimension must be contiguous")
+    if (T is not None and a != T) or (H is not None and b != H) or (d is not None and c != d):
+        raise ValueError(f"{name}: {(a, b, c)} where {(T, H, d)} is expected")
+    return TmTensor(x.data_ptr(), a, b, c, st, sh)
+
+
+def _int32(t, name, dev, n=None):
+    """Device address of a contiguous int32 vector of at least n elements (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name}: contiguous int32 vector on {dev} expected")
+    if n is not None and t.shape[0] < n:
+        raise ValueError(f"{name}: at least {n} elements expected, got {t.shape[0]}")
+    return t.data_ptr()
+
+
+def _weight(w, name, dev, d):
+    if w is None:
+        return None
+    if w.dtype != torch.float16 or w.shape != (d,) or not w.is_contiguous() or w.device != dev:
+        raise ValueError(f"{name}: contiguous fp16 [{d}] on {dev} expected")
+    return w.data_ptr()
+
+
+def _table(block_table, kv, batch=None):
+    """(address, row stride, columns, rows) of an int32 [batch, columns] block table."""
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.device != kv.device:
+        raise ValueError(f"block_table: int32 [batch, columns] on {kv.device} expected")
+    n, cols = block_table.shape
+    if n < 1 or cols < 1 or (cols > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table: at least one row and column, columns contiguous")
+    if batch is not None and n < batch:
+        raise ValueError(f"block_table: {batch} rows expected, got {n}")
+    return block_table.data_ptr(), block_table.stride(0), cols, n
+
+
+def _refs(*structs):
+    return tuple(None if s is None else ctypes.byref(s) for s in structs)
+
+
+def _rope_call(name, q, k, out, rope, positions, pos_offset, *weights):
+    dev = q.device
+    T, d = q.shape[0], q.shape[2]
+    if rope is not None and rope.d != d:
+        raise ValueError(f"rope is for heads of {rope.d}, q has {d}")
+    if out is None:
+        out = (torch.empty(q.shape, dtype=q.dtype, device=dev),
+               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=dev))
+    elif isinstance(out, torch.Tensor):
+        out = (out, None)
+    qo, ko = out
+    if k is not None and ko is None:
+        raise ValueError("out: a pair (q, k) expected")
+    qd, qod = _thd(q, "q", dev), _thd(qo, "q out", dev, T, q.shape[1], d)
+    kd = kod = None
+    if k is not None:
+        kd, kod = _thd(k, "k", dev, T, None, d), _thd(ko, "k out", dev, T, k.shape[1], d)
+    _call(dev, name, *_refs(qd, kd, qod, kod), *weights, None if rope is None else rope._ref,
+          _int32(positions, "positions", dev, T), int(pos_offset))
+    return qo if k is None else (qo, ko)
+
+
+def rope(q, k=None, *, rope, positions=None, pos_offset=0, out=None):
+    """Rotary positions (tm_rope) of q, and of k in the same launch: fp16 [T,
+    H, d], row t at position positions[t] + pos_offset (int32 [T]), or t +
+    pos_offset without positions.  out: tensors to write, (q, k) themselves
+    for in place.  Returns the rotated q, or (q, k)."""
+    if rope is None:
+        raise ValueError("rope: a Rope expected")
+    return _rope_call("tm_rope", q, k, out, rope, positions, pos_offset)
+
+
+def qk_norm_rope(q, k=None, *, q_weight, k_weight=None, eps=1e-6, rope=None, positions=None, pos_offset=0, out=None):
+    """Norm of each head of q (and k), x / sqrt(mean(x^2) + eps) * weight
+    (fp16 [d]), and the rotation, in one pass (tm_qk_norm_rope); rope None:
+    the norm alone.  Other arguments as for rope()."""
+    if q_weight is None or (k is not None and k_weight is None):
+        raise ValueError("a weight for each of q and k expected")
+    d = q.shape[2]
+    return _rope_call("tm_qk_norm_rope", q, k, out, rope, positions, pos_offset,
+                      _weight(q_weight, "q_weight", q.device, d),
+                      _weight(k_weight if k is not None else None, "k_weight", q.device, d), float(eps))
+
+
+def block_table_check(block_table, kv_lens, num_pages, page_size):
+    """Raises ValueError where a host block table (int32 [batch, columns])
+    does not hold kv_lens[b] tokens of each sequence in pages 0 ..
+    num_pages - 1 (tm_block_table_check): the test that the kernels make of
+    each page, before anything is launched."""
+    t = torch.as_tensor(block_table, dtype=torch.int32, device="cpu").contiguous()
+    n = torch.as_tensor(kv_lens, dtype=torch.int32, device="cpu").contiguous()
+    if t.dim() != 2 or n.dim() != 1 or n.shape[0] > t.shape[0]:
+        raise ValueError("block_table [batch, columns] and kv_lens [batch] expected")
+    bad = (ctypes.c_int32 * 2)(-1, -1)
+    st = _lib().tm_block_table_check(t.data_ptr(), t.shape[1], t.shape[1], n.data_ptr(), n.shape[0], int(num_pages),
+                                     int(page_size), bad)
+    if st == TM_ERR_INVALID_ARG and bad[0] >= 0:
+        raise ValueError(f"block_table: sequence {bad[0]}, column {bad[1]}: no usable page")
+    _check(st, "tm_block_table_check")
+
+
+def kv_append(k, v, kv, block_table, kv_lens, *, cu_seqlens=None, rope=None, pos_offset=0, k_weight=None, q=None,
+              q_weight=None, eps=1e-6, q_out=None):
+    """New tokens' k and v (fp16 [T, Hkv, d]) into the pages of kv, K normed
+    (k_weight) and rotated (rope) on the way, and their queries q normed and
+    rotated in the same launch (tm_kv_append).  kv_lens: int32 [batch], each
+    sequence's own length AFTER the append; rows are packed by cu_seqlens
+    (int32 [batch + 1]) or T / batch for each sequence.  pos_offset: length of
+    a shared prefix.  Returns q_out (a new tensor if not given), or None
+    without q."""
+    dev = kv.device
+    T = k.shape[0]
+    batch = kv_lens.shape[0]
+    ptr, stride, cols, _ = _table(block_table, kv, batch)
+    if cu_seqlens is None and T % max(batch, 1):
+        raise ValueError(f"{T} rows for {batch} sequences: cu_seqlens expected")
+    if rope is not None and rope.d != kv.d:
+        raise ValueError(f"rope is for heads of {rope.d}, the cache holds {kv.d}")
+    kd, vd = _thd(k, "k", dev, T, kv.H, kv.d), _thd(v, "v", dev, T, kv.H, kv.d)
+    qd = qod = None
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        qd, qod = _thd(q, "q", dev, T, None, kv.d), _thd(q_out, "q_out", dev, T, q.shape[1], kv.d)
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight come with q")
+    _call(dev, "tm_kv_append", *_refs(kd, vd), kv._ref, ptr, stride, cols, _int32(kv_lens, "kv_lens", dev),
+          _int32(cu_seqlens, "cu_seqlens", dev, batch + 1), batch, None if rope is None else rope._ref, int(pos_offset),
+          *_refs(qd, qod), _weight(q_weight, "q_weight", dev, kv.d), _weight(k_weight, "k_weight", dev, kv.d),
+          float(eps))
+    return q_out
+
+
+def kv_gather(kv, block_table, cu_seqlens_k, *, out):
+    """The cached rows of each sequence as contiguous fp16 (tm_kv_gather): out
+    = (k, v) [T, Hkv, d], rows cu_seqlens_k[b] .. cu_seqlens_k[b + 1] (int32
+    [batch + 1]) sequence b's tokens in order: the keys and values of attn_fwd
+    with cu_seqlens_k.  Returns out."""
+    k, v = out
+    dev = kv.device
+    batch = cu_seqlens_k.shape[0] - 1
+    if batch < 1:
+        raise ValueError("cu_seqlens_k: int32 [batch + 1] expected")
+    ptr, stride, cols, _ = _table(block_table, kv, batch)
+    kd, vd = _thd(k, "k", dev, None, kv.H, kv.d), _thd(v, "v", dev, k.shape[0], kv.H, kv.d)
+    _call(dev, "tm_kv_gather", kv._ref, ptr, stride, cols, _int32(cu_seqlens_k, "cu_seqlens_k", dev), batch,
+          *_refs(kd, vd))
+    return out
+
+
+def shared_prefix_workspace_bytes(kv, batch, T, Hq, *, max_seqlen=None, prefix_len=0, max_kv_len):
+    """Bytes of the workspace attn_shared_prefix needs for these sizes."""
+    n = int(_lib().tm_attn_shared_prefix_workspace(int(T), int(Hq), kv.H, kv.d, int(batch),
+                                                   int(-(-T // batch) if max_seqlen is None else max_seqlen),
+                                                   int(prefix_len), int(max_kv_len)))
+    if n < 0:
+        raise ValueError("bad sizes")
+    return n
+
+
+def attn_shared_prefix(q, kv, block_table, kv_lens, *, prefix_pages=None, prefix_len=0, cu_seqlens=None,
+                       max_seqlen=None, max_kv_len=None, causal=True, workspace=None, out=None):
+    """Attention of a batch over a paged cache (tm_attn_shared_prefix): q fp16
+    [T, Hq, d], packed by cu_seqlens (int32 [batch + 1]; max_seqlen bounds the
+    rows of a sequence) or T / batch rows each.  Every row sees the prefix_len
+    tokens in prefix_pages (int32), read once for the whole batch, and, bottom-right
+    causal, its sequence's own kv_lens[b] tokens (int32 [batch]) in
+    block_table's pages.  max_kv_len: a bound on kv_lens (default: what the
+    table holds) that sizes the launch, so it may stay while a captured graph's
+    kv_lens grow.  workspace: uint8, shared_prefix_workspace_bytes(...), one
+    for each call that may run at the same time; allocated here when None.
+    Returns out (a new tensor if not given)."""
+    dev = kv.device
+    T, Hq = q.shape[0], q.shape[1]
+    batch = kv_lens.shape[0]
+    if batch < 1:
+        raise ValueError("kv_lens: int32 [batch] expected")
+    ptr, stride, cols, _ = _table(block_table, kv, batch)
+    if max_kv_len is None:
+        max_kv_len = cols * kv.page_size
+    if cu_seqlens is None:
+        if T % batch:
+            raise ValueError(f"{T} rows for {batch} sequences: cu_seqlens expected")
+        max_seqlen = T // batch
+    elif max_seqlen is None:
+        raise ValueError("max_seqlen comes with cu_seqlens")
+    if Hq % kv.H:
+        raise ValueError(f"{Hq} query heads over {kv.H} K/V heads")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(shared_prefix_workspace_bytes(kv, batch, T, Hq, max_seqlen=max_seqlen,
+                                                              prefix_len=prefix_len, max_kv_len=max_kv_len),
+                                dtype=torch.uint8, device=dev)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError(f"workspace: contiguous uint8 on {dev} expected")
+    qd, od = _thd(q, "q", dev, T, Hq, kv.d), _thd(out, "out", dev, T, Hq, kv.d)
+    _call(dev, "tm_attn_shared_prefix", *_refs(qd), kv._ref, *_refs(od), ptr, stride, cols,
+          _int32(kv_lens, "kv_lens", dev), _int32(cu_seqlens, "cu_seqlens", dev, batch + 1), batch, int(max_seqlen),
+          _int32(prefix_pages, "prefix_pages", dev, -(-int(prefix_len) // kv.page_size)) if prefix_len else None,
+          int(prefix_len), int(max_kv_len), int(bool(causal)), workspace.data_ptr(), workspace.numel())
     return out
 
 
