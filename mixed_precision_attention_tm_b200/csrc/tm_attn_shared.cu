@@ -8,7 +8,6 @@
 #include <atomic>
 
 #include "tm_attn_shared.cuh"
-#include "tm_host.h"
 
 namespace tmk {
 
@@ -16,19 +15,41 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t ba
                        int64_t prefix_len, int64_t max_kv_len) {
   SharedPlan p{};
   p.group = Hq / Hkv;
-  const int64_t own_rows = (max_seqlen * p.group + 15) / 16, pre_rows = (T * p.group + 15) / 16;
-  const int64_t own_units = (max_kv_len + 127) / 128, pre_units = (prefix_len + 127) / 128;
-  const int64_t units = batch * own_rows * Hkv * own_units + pre_rows * Hkv * pre_units;
-  // two waves of one CTA per SM, every CTA with about the same keys
-  int64_t chunk = (units + 2 * kSmsB200 - 1) / (2 * kSmsB200);
-  const int64_t most = own_units > pre_units ? own_units : pre_units;
-  if (chunk < (most + 31) / 32) chunk = (most + 31) / 32;   // at most 32 splits of each
-  if (chunk < 1) chunk = 1;
+  const int64_t own_packed = max_seqlen * p.group, pre_packed = T * p.group;
+  p.own_tile = own_packed > kSplitRowsOwn;
+  p.pre_tile = prefix_len > 0 && pre_packed > kSplitRowsPrefix;
+  const int64_t own_rows = ceil_div(own_packed, p.own_tile ? 256 : 16);
+  const int64_t pre_rows = ceil_div(pre_packed, p.pre_tile ? 256 : 16);
+  const int64_t own_units = ceil_div(max_kv_len, 128), pre_units = ceil_div(prefix_len, 128);
   p.own_rows = static_cast<int>(own_rows);
   p.pre_rows = static_cast<int>(pre_rows);
-  p.own_chunk = p.pre_chunk = static_cast<int>(chunk * 128);
-  p.own_splits = static_cast<int>((own_units + chunk - 1) / chunk);
-  p.pre_splits = static_cast<int>((pre_units + chunk - 1) / chunk);
+  // split kernel: two waves of one CTA per SM, every CTA with about the same keys, at most 30 splits of each
+  const int64_t split_units = (p.own_tile ? 0 : batch * own_rows * Hkv * own_units) +
+                              (p.pre_tile ? 0 : pre_rows * Hkv * pre_units);
+  int64_t chunk = ceil_div(split_units, 2 * kSmsB200);
+  if (chunk < 1) chunk = 1;
+  if (p.pre_tile) {
+    // equal pieces of the line of key tiles, one for each SM
+    const int64_t line = Hkv * pre_rows * pre_units;
+    int64_t c = ceil_div(line, kSmsB200);
+    if (c < ceil_div(pre_units, kMostSplits)) c = ceil_div(pre_units, kMostSplits);
+    if (c > line) c = line;
+    if (c < 1) c = 1;
+    p.pre_tiles = static_cast<int>(pre_units);
+    p.pre_chunk = static_cast<int>(c);
+    p.pre_ctas = static_cast<int>(ceil_div(line, c));
+    p.pre_splits = static_cast<int>(line <= c ? 1 : (pre_units % c == 0 ? pre_units / c : ceil_div(pre_units - 1, c) + 1));
+  } else {
+    const int64_t c = chunk > ceil_div(pre_units, kMostSplits) ? chunk : ceil_div(pre_units, kMostSplits);
+    p.pre_chunk = static_cast<int>((c < 1 ? 1 : c) * 128);
+    p.pre_splits = static_cast<int>(ceil_div(pre_units, c < 1 ? 1 : c));
+  }
+  int64_t c = p.own_tile ? ceil_div(batch * own_rows * Hkv * own_units, 2 * kSmsB200) : chunk;
+  if (p.own_tile && c < 4) c = 4;
+  if (c < ceil_div(own_units, kMostSplits)) c = ceil_div(own_units, kMostSplits);
+  if (c < 1) c = 1;
+  p.own_chunk = static_cast<int>(c * 128);
+  p.own_splits = static_cast<int>(ceil_div(own_units, c));
   p.slots = p.own_splits + p.pre_splits;
   const int64_t rows = T * Hq;
   p.ml_bytes = (p.slots * rows * 8 + 255) / 256 * 256;
@@ -43,14 +64,6 @@ constexpr int kWarps = 4;
 constexpr int kStep = 32;     // keys of one warp step
 constexpr int kStages = 3;
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -69,23 +82,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
-}
-
-// Two codes, as bytes code + 128 picked by `sel` from w, to a pair of fp16:
-// under the exponent byte 0x64 a byte b reads as 1024 + b, exactly.
-__device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sel) {
-  const uint32_t x = __byte_perm(w, 0x64646464u, sel);
-  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(1152.0f));
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // Bytes of one 32-key stage of K (V the same), and where the 16-byte piece c
@@ -129,7 +129,7 @@ constexpr int split_smem() {
 // lane's 16 consecutive codes serve four MMAs; the order of output columns is
 // free too, so a lane's n index stands for d / 8 consecutive dimensions.
 template <int D, bool INT8>
-__global__ void __launch_bounds__(kWarps * 32) split_kernel(const __grid_constant__ SharedArgs a, DevErr err) {
+__device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
   using S = Stage<D, INT8>;
   constexpr int NT = D / 8, KS = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kWarps * 32) split_kernel(const __grid_constan
   int64_t item = blockIdx.x;
   const int kvh = static_cast<int>(item % H);
   item /= H;
-  const int64_t pre_items = static_cast<int64_t>(p.pre_splits) * p.pre_rows;
+  const int64_t pre_items = p.pre_tile ? 0 : static_cast<int64_t>(p.pre_splits) * p.pre_rows;
   const bool prefix = item < pre_items;
   int b = 0, slot;
   int64_t row0, start = 0, nrows, k0, k1, hidden = 0;   // hidden: own keys that row 0's token does not see
@@ -546,6 +546,13 @@ __global__ void __launch_bounds__(kWarps * 32) split_kernel(const __grid_constan
   }
 }
 
+template <int D, bool INT8>
+__global__ void __launch_bounds__(kWarps * 32) split_kernel(const __grid_constant__ SharedArgs a, DevErr err) {
+  pdl_launch_dependents();
+  split_rows<D, INT8>(a, err);
+  pdl_wait();      // whoever waits for this kernel has waited for the one before it
+}
+
 // Joins a row's splits: one warp per (token, query head), the slots' (m, l)
 // across the lanes, then the O rows that carry weight.
 template <int D>
@@ -558,11 +565,23 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Share
   const int64_t t = row / Hq;
   if (t >= rows_in_use(a) || (a.cu != nullptr && t < __ldg(a.cu))) return;
   constexpr int V = D / 32;
+  const SharedPlan& p = a.plan;
+  // prefix results of this row: the pieces of the line that its row block's key tiles lie in
+  int pre = p.pre_splits;
+  if (p.pre_tile) {
+    const int h = static_cast<int>(row - t * Hq);
+    const int64_t packed = t * p.group + h % p.group;
+    const int64_t first = (static_cast<int64_t>(h / p.group) * p.pre_rows + packed / 256) * p.pre_tiles;
+    pre = static_cast<int>((first + p.pre_tiles - 1) / p.pre_chunk - first / p.pre_chunk) + 1;
+  }
+  const int count = pre + p.own_splits;
+  pdl_wait();
   float acc[V] = {}, M = -INFINITY, L = 0.f;
-  for (int s0 = 0; s0 < a.plan.slots; s0 += 32) {
-    const int n = a.plan.slots - s0 < 32 ? a.plan.slots - s0 : 32;
+  for (int s0 = 0; s0 < count; s0 += 32) {
+    const int n = count - s0 < 32 ? count - s0 : 32;
+    const int own_at = p.pre_splits - pre;      // result i lies in slot i, or i + own_at from `pre` on
     float2 ml = make_float2(-INFINITY, 0.f);
-    if (lane < n) ml = a.ml[(s0 + lane) * total + row];
+    if (lane < n) ml = a.ml[(s0 + lane + (s0 + lane < pre ? 0 : own_at)) * total + row];
     float mx = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -582,7 +601,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Share
       const int s = __ffs(live) - 1;
       live &= live - 1;
       const float ws = __shfl_sync(0xffffffffu, w, s);
-      const float* src = a.o + ((s0 + s) * total + row) * D + lane * V;
+      const int slot = s0 + s + (s0 + s < pre ? 0 : own_at);
+      const float* src = a.o + (slot * total + row) * D + lane * V;
       if (V == 4) {
         const float4 f = *reinterpret_cast<const float4*>(src);
         acc[0] += ws * f.x;
@@ -606,33 +626,39 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Share
 }
 
 template <int D, bool INT8>
-tm_status launch(const SharedArgs& a, DevErr err, cudaStream_t stream) {
+tm_status launch_split(const SharedArgs& a, bool overlap, DevErr err, cudaStream_t stream) {
   constexpr int smem = split_smem<D, INT8>();
-  static std::atomic<uint64_t> prepared{0};     // devices whose kernel has its shared memory
-  int dev = 0;
-  tm_status st = check_cuda(cudaGetDevice(&dev));
+  static std::atomic<uint64_t> prepared{0};
+  const tm_status st = prepare_smem(split_kernel<D, INT8>, smem, prepared);
   if (st != TM_OK) return st;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(prepared.load(std::memory_order_relaxed) & bit)) {
-    st = check_cuda(cudaFuncSetAttribute(split_kernel<D, INT8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    if (st != TM_OK) return st;
-    prepared.fetch_or(bit, std::memory_order_relaxed);
-  }
   const SharedPlan& p = a.plan;
-  const int64_t items = (static_cast<int64_t>(p.pre_splits) * p.pre_rows +
-                         static_cast<int64_t>(p.own_splits) * a.batch * p.own_rows) * a.pool.H;
-  if (items > 0x7fffffff) return TM_ERR_UNSUPPORTED;
-  if (items > 0) {
-    split_kernel<D, INT8><<<static_cast<unsigned>(items), kWarps * 32, smem, stream>>>(a, err);
-    st = check_cuda(cudaGetLastError());
-    if (st != TM_OK) return st;
+  const int64_t items = ((p.pre_tile ? 0 : static_cast<int64_t>(p.pre_splits) * p.pre_rows) +
+                         (p.own_tile ? 0 : static_cast<int64_t>(p.own_splits) * a.batch * p.own_rows)) * a.pool.H;
+  return launch_kernel(split_kernel<D, INT8>, items, kWarps * 32, smem, overlap, stream, a, err);
+}
+
+// Up to three kernels, each allowed to start while the one before it drains:
+// none of the first two reads what the other writes, the join waits for both.
+tm_status launch(const SharedArgs& a, int d, bool int8, DevErr err, cudaStream_t stream) {
+  const SharedPlan& p = a.plan;
+  bool after = false;
+  tm_status st = TM_OK;
+  if (p.pre_tile) {
+    st = shared_tile(a, d, int8, true, after, err, stream);
+    after = true;
   }
-  if (p.slots == 1) return TM_OK;
-  const int64_t rows = a.T * a.pool.H * p.group;
-  const int64_t blocks = (rows + 7) / 8;
-  if (blocks > 0x7fffffff) return TM_ERR_UNSUPPORTED;
-  join_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
-  return check_cuda(cudaGetLastError());
+  if (st == TM_OK && p.own_tile && p.own_splits > 0) {
+    st = shared_tile(a, d, int8, false, after, err, stream);
+    after = true;
+  }
+  if (st == TM_OK && ((!p.pre_tile && p.pre_splits > 0) || (!p.own_tile && p.own_splits > 0))) {
+    st = d == 128 ? (int8 ? launch_split<128, true>(a, after, err, stream) : launch_split<128, false>(a, after, err, stream))
+                  : (int8 ? launch_split<64, true>(a, after, err, stream) : launch_split<64, false>(a, after, err, stream));
+    after = true;
+  }
+  if (st != TM_OK || p.slots == 1) return st;
+  const int64_t blocks = (a.T * a.pool.H * p.group + 7) / 8;
+  return launch_kernel(d == 128 ? join_kernel<128> : join_kernel<64>, blocks, 256, 0, after, stream, a);
 }
 
 bool plan_args_ok(int64_t T, int32_t Hq, int32_t Hkv, int32_t batch, int64_t max_seqlen, int64_t prefix_len,
@@ -704,6 +730,5 @@ extern "C" tm_status tm_attn_shared_prefix(const tm_tensor* q, const tm_paged_kv
   const DevErr err{device_error_word()};
   if (err.word == nullptr) return cuda_fail(static_cast<int>(cudaErrorInvalidSymbol));
   cudaStream_t s = as_stream(stream);
-  if (d == 128) return int8 ? launch<128, true>(a, err, s) : launch<128, false>(a, err, s);
-  return int8 ? launch<64, true>(a, err, s) : launch<64, false>(a, err, s);
+  return launch(a, static_cast<int>(d), int8, err, s);
 }

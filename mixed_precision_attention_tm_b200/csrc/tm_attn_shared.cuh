@@ -12,6 +12,9 @@
 //   out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,  M = max m_i.
 #pragma once
 
+#include <atomic>
+
+#include "tm_host.h"
 #include "tm_paged.cuh"
 
 namespace tmk {
@@ -24,14 +27,24 @@ constexpr int kSmsB200 = 148;
 // values fp16 holds) multiplied in, below fp16's 65504.
 constexpr float kPOffset = 6.0f;
 
+// Rows (of a sequence, of the batch) up to which the split-key kernel takes
+// the own tokens or the prefix; more rows go to the tile kernel.
+constexpr int kSplitRowsOwn = 64, kSplitRowsPrefix = 16;
+constexpr int kMostSplits = 30;
+
 struct SharedPlan {
   int group;                  // query heads per K/V head
-  int own_rows, pre_rows;     // row blocks (of 16 rows) per sequence, of the batch
-  int own_splits, pre_splits;
-  int own_chunk, pre_chunk;   // keys per split
+  int own_tile, pre_tile;     // 1: on the tile kernel (256-row blocks), 0: on the split-key kernel (16-row blocks)
+  int own_rows, pre_rows;     // row blocks per sequence, of the batch
+  int own_splits, pre_splits; // most results of a row
+  int own_chunk;              // keys per split
+  int pre_chunk;              // the same; on the tile kernel: key tiles per CTA
+  int pre_tiles, pre_ctas;    // tile kernel: key tiles of the prefix, CTAs
   int slots;                  // own_splits + pre_splits
   int64_t ml_bytes, bytes;    // workspace: (m, l) of every slot and row, then O
 };
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t batch, int64_t max_seqlen,
                        int64_t prefix_len, int64_t max_kv_len);
@@ -66,5 +79,72 @@ __device__ __forceinline__ int64_t rows_in_use(const SharedArgs& a) {
   const int64_t n = a.cu != nullptr ? static_cast<int64_t>(__ldg(a.cu + a.batch)) : a.T;
   return n < a.T ? n : a.T;
 }
+
+// A kernel may be launched while the one before it in the stream still runs
+// (after that one's pdl_launch_dependents); pdl_wait returns when that one has
+// ended and its writes are visible.
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Two codes, as bytes code + 128 picked by `sel` from w, to a pair of fp16:
+// under the exponent byte 0x64 a byte b reads as 1024 + b, exactly.
+__device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sel) {
+  const uint32_t x = __byte_perm(w, 0x64646464u, sel);
+  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(1152.0f));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Dynamic shared memory of a kernel, allowed once for each device.
+template <typename K>
+tm_status prepare_smem(K kernel, int smem, std::atomic<uint64_t>& prepared) {
+  int dev = 0;
+  tm_status st = check_cuda(cudaGetDevice(&dev));
+  if (st != TM_OK) return st;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (prepared.load(std::memory_order_relaxed) & bit) return TM_OK;
+  st = check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  if (st == TM_OK) prepared.fetch_or(bit, std::memory_order_relaxed);
+  return st;
+}
+
+// overlap: the kernel may start before the previous one of the stream has ended.
+template <typename... P, typename... A>
+tm_status launch_kernel(void (*kernel)(P...), int64_t blocks, int threads, int smem, bool overlap, cudaStream_t stream,
+                        const A&... args) {
+  if (blocks > 0x7fffffff) return TM_ERR_UNSUPPORTED;
+  if (blocks <= 0) return TM_OK;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return check_cuda(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
+// tm_attn_shared_tile.cu: the prefix's (or the own tokens') part on the tile kernel.
+tm_status shared_tile(const SharedArgs& a, int d, bool int8, bool prefix, bool overlap, DevErr err,
+                      cudaStream_t stream);
 
 }  // namespace tmk

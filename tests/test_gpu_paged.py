@@ -467,3 +467,9 @@ def test_offsets_past_32_bits():
     near = i32([[3, 0], [1, 2]])
     ops.kv_append(k, v, small, near, i32(lens), cu_seqlens=offsets(lens))
     assert torch.equal(out, ops.attn_shared_prefix(q, small, near, i32(lens)))
+
+
+@pytest.mark.parametrize("d,int8", [(128, False), (64, True), (128, True), (64, False)])
+def test_attention_pieces_across_row_blocks(d, int8):
+    """More key tiles of the prefix than SMs, in pieces that end inside row blocks; ragged own rows of several tiles."""
+    attend(41, [260, 90, 2], [110, 90, 1], 2500, d, 32, 16, 4, int8)
