@@ -41,6 +41,13 @@ constexpr int kThreads = 512;
 // up to 2^kLazy above it are left alone: 2^15 at most, inside fp16.
 constexpr float kLazy = 15.0f - kPOffset;
 
+// Of every 8 pairs of exponentials, how many run on the FMA pipe: the special
+// function unit alone takes as long as the MMAs of a tile.
+#ifndef TM_FMA_PAIRS
+#define TM_FMA_PAIRS 3
+#endif
+constexpr int kFmaPairs = TM_FMA_PAIRS;
+
 template <int D>
 struct CfgT {
   static constexpr int BM = 128, BN = 128;
@@ -71,7 +78,8 @@ enum {
   T_DRAIN = 8,    // +2
   T_FULL = 10,    // +NSLOT
   T_EMPTY = 18,   // +NSLOT
-  T_COUNT = 26
+  T_OLAST = 26,   // +2: a segment's last P.V (T_ODONE's parity cannot tell it from the one two before)
+  T_COUNT = 28
 };
 // Named barriers: NB_P + t softmax t -> issuer t (P stored); NB_KV + t wait
 // helper -> issuer t (operands landed); NB_START softmax A -> issuer B.
@@ -85,6 +93,29 @@ struct Segment {
   int64_t hidden;             // own, causal: token i of the sequence sees keys below hidden + i
   int nj[2];                  // key tiles that each query tile sees
 };
+
+// 2^y for y <= 15 on the FMA pipe, two lanes at a time: y = n + f, n = rne(y)
+// by adding 1.5 * 2^23, 2^f by a degree-4 minimax polynomial on [-1/2, 1/2]
+// (relative error below 2^-18 with its fp32 roundings; coefficients from a Remez
+// exchange), n into the exponent field.  y is clamped at -125, so that masked
+// scores give 2^-125, which is 0 in fp16 and nothing in a row's sum.
+__device__ __forceinline__ void exp2_fma2(uint64_t y2, float& p0, float& p1) {
+  float y0, y1;
+  f2unpack(y2, y0, y1);
+  y2 = f2pack(fmaxf(y0, -125.0f), fmaxf(y1, -125.0f));
+  const uint64_t t2 = f2add(y2, f2pack(12582912.0f, 12582912.0f));
+  const uint64_t n2 = f2add(t2, f2pack(-12582912.0f, -12582912.0f));
+  const uint64_t f2 = f2fma(n2, f2pack(-1.0f, -1.0f), y2);
+  uint64_t q = f2fma(f2pack(0.009570102f, 0.009570102f), f2, f2pack(0.05591786f, 0.05591786f));
+  q = f2fma(q, f2, f2pack(0.24024744f, 0.24024744f));
+  q = f2fma(q, f2, f2pack(0.6931218f, 0.6931218f));
+  q = f2fma(q, f2, f2pack(0.9999993f, 0.9999993f));
+  float q0, q1, t0, t1;
+  f2unpack(q, q0, q1);
+  f2unpack(t2, t0, t1);
+  p0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
+  p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
+}
 
 template <int D, bool INT8>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ SharedArgs a, int prefix,
@@ -182,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(T_ODONE + t), 1);
       mbar_init(bar(T_DRAIN + t), 1);
+      mbar_init(bar(T_OLAST + t), 1);
     }
     for (int s = 0; s < C::NSLOT; ++s) {
       mbar_init(bar(T_FULL + s), 4);
@@ -260,92 +292,105 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       ++np;
     };
     uint32_t n = 0, qn = 0;
+    const int64_t st = a.pool.stride_t;
+    const int c = lane % PIECES, sub = lane / PIECES;
     while (next_segment(u, sg)) {
       const int nj = sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
       if (nj == 0) continue;
-      // this lane's row of key tile j: where it lies, and its scales
-      auto look_up = [&](int j, int64_t& off, float& ks, float& vs) {
-        const int64_t key = sg.key0 + static_cast<int64_t>(j) * 128 + 32 * w + lane;
-        off = -1;
-        ks = 0.f;
-        vs = 0.f;
-        if (j >= nj || key >= sg.lk) return;
-        int32_t page;
-        if (prefix) {
-          page = __ldg(a.prefix_pages + (key >> shift));
-          if (!page_ok(page, a.pool.num_pages)) page = -1;
-        } else {
-          page = page_of(a.pt, sg.b, key);
-        }
-        if (page < 0) {
-          dev_error(err, TM_DEVERR_SEQLEN);
-          return;
-        }
-        off = page * a.pool.stride_page + (key & page_mask) * a.pool.stride_t;
-        if (INT8) {
-          const int64_t so = page * a.pool.sstride_page + (key & page_mask) * a.pool.sstride_t +
-                             sg.kvh * a.pool.sstride_h;
-          ks = __half2float(a.pool.ks[so]);
-          vs = __half2float(a.pool.vs[so]);
-        }
+      const uint8_t* kbase = a.pool.k + sg.kvh * a.pool.stride_h + c * 16;
+      const uint8_t* vbase = a.pool.v + sg.kvh * a.pool.stride_h + c * 16;
+      const int64_t first = sg.key0 + 32 * w;        // this warp's first key of tile 0
+      // Pages of this warp's two runs of 16 keys of key tile j (a run never crosses a page), -1 where there is
+      // nothing to read.  Loaded one tile ahead.
+      auto page_at = [&](int j, int run) -> int32_t {
+        const int64_t key = first + static_cast<int64_t>(j) * 128 + 16 * run;
+        if (j >= nj || key >= sg.lk) return -1;
+        const int64_t col = key >> shift;
+        if (prefix) return __ldg(a.prefix_pages + col);
+        return col < a.pt.cols ? __ldg(a.pt.table + sg.b * a.pt.stride + col) : -2;
       };
-      auto copy_rows = [&](uint32_t tile, const uint8_t* base, int64_t off) {
-        const int c = lane % PIECES;
+      // Copies this warp's rows of one tile; base[run]: the run's first row, valid[run]: its rows to read
+      auto copy_rows = [&](uint32_t tile, const uint8_t* base, const int64_t (&off)[2], const int (&valid)[2]) {
 #pragma unroll
-        for (int i = 0; i < 32 / RPI; ++i) {
-          const int src = i * RPI + lane / PIECES;
-          const int r = 32 * w + src;
-          const int64_t o = __shfl_sync(0xffffffffu, off, src);
-          const bool real = o >= 0;
-          const uint32_t dst = tile + (INT8 ? CODE_OFF : (c >> 3) * C::HALF) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-          cp16(dst, base + (real ? o + c * 16 : 0), real);
+        for (int run = 0; run < 2; ++run) {
+          const uint8_t* src = base + off[run];
+#pragma unroll
+          for (int i = 0; i < 16 / RPI; ++i) {
+            const int rr = i * RPI + sub;
+            const int r = 32 * w + 16 * run + rr;
+            const uint32_t dst = tile + (INT8 ? CODE_OFF : (c >> 3) * C::HALF) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            const bool real = rr < valid[run];
+            cp16(dst, real ? src + rr * st : base, real);
+          }
         }
       };
-      int64_t off;
-      float ks, vs;
-      look_up(0, off, ks, vs);
+      int32_t page[2] = {page_at(0, 0), page_at(0, 1)};
       // Q of both tiles, once the MMAs of the last segment have read theirs
       if (np == 3) finish_oldest();
       if (qn > 0) acquire(bar(T_QEMPTY), (qn - 1) & 1);
       ++qn;
       {
         constexpr int QP = D / 8;
-        const int c = lane % QP;
-#pragma unroll 1
+        const int qc = lane % QP;
+        const uint32_t row0 = static_cast<uint32_t>(sg.row0), gg = static_cast<uint32_t>(g);
+        const __half* qbase = a.q + sg.start * a.q_t + static_cast<int64_t>(sg.kvh) * g * a.q_h + qc * 8;
+#pragma unroll 4
         for (int i = 0; i < 2 * QP; ++i) {      // 64 rows of this warp, 32 / QP at a time
           const int k = i * (32 / QP) + lane / QP;
           const int t = k >> 5, r = 32 * w + (k & 31);
           const int pr = 128 * t + r;
           const bool real = pr < sg.rows;
-          const int64_t row = sg.row0 + pr;
-          const __half* src = real ? a.q + (sg.start + row / g) * a.q_t + (sg.kvh * g + row % g) * a.q_h + c * 8 : a.q;
-          cp16(sbase + t * C::Q_BYTES + (c >> 3) * C::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, real);
+          const uint32_t row = row0 + pr, tok = row / gg;
+          const __half* src = real ? qbase + tok * a.q_t + (row - tok * gg) * a.q_h : a.q;
+          cp16(sbase + t * C::Q_BYTES + (qc >> 3) * C::HALF + r * 128 + (((qc & 7) ^ (r & 7)) << 4), src, real);
         }
         pushed(bar(T_QFULL), 0);
       }
+      float nks = 0.f, nvs = 0.f;      // INT8: scales of this lane's key, loaded while K is copied
       for (int j = 0; j < nj; ++j, ++n) {
-        int64_t noff;
-        float nks, nvs;
-        look_up(j + 1, noff, nks, nvs);
+        int64_t off[2];
+        int valid[2];
+#pragma unroll
+        for (int run = 0; run < 2; ++run) {
+          const int64_t key = first + static_cast<int64_t>(j) * 128 + 16 * run;
+          const int64_t left = sg.lk - key;
+          bool use = left > 0;
+          if (use && !page_ok(page[run], a.pool.num_pages)) {
+            if (lane == 0) dev_error(err, TM_DEVERR_SEQLEN);
+            use = false;
+          }
+          valid[run] = use ? (left < 16 ? static_cast<int>(left) : 16) : 0;
+          off[run] = use ? page[run] * a.pool.stride_page + (key & page_mask) * a.pool.stride_t : 0;
+        }
+        if (INT8) {
+          const int run = lane >> 4;
+          const int64_t key = first + static_cast<int64_t>(j) * 128 + lane;
+          nks = nvs = 0.f;
+          if ((lane & 15) < valid[run]) {
+            const int64_t so = page[run] * a.pool.sstride_page + (key & page_mask) * a.pool.sstride_t +
+                               sg.kvh * a.pool.sstride_h;
+            nks = __half2float(a.pool.ks[so]);
+            nvs = __half2float(a.pool.vs[so]);
+          }
+        }
+        page[0] = page_at(j + 1, 0);
+        page[1] = page_at(j + 1, 1);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const uint32_t i = 2 * n + v, slot = i % C::NSLOT, lap = i / C::NSLOT;
           if (lap > 0) acquire(bar(T_EMPTY + slot), (lap - 1) & 1);
           else if (np == 3) finish_oldest();
           const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT;
-          copy_rows(tile, (v ? a.pool.v : a.pool.k) + sg.kvh * a.pool.stride_h, off);
+          copy_rows(tile, v ? vbase : kbase, off, valid);
           if (INT8 && v) {      // the V tile's release frees its stage of scales
             float* s = scales + (slot >> 1) * 384 + 32 * w + lane;
-            const float f = vs == 0.f ? 5.9604645e-8f : vs;   // a zero scale (codes all 0) counts in the row sum alone
-            s[0] = ks * a.scale_log2;
+            const float f = nvs == 0.f ? 5.9604645e-8f : nvs;   // a zero scale (codes all 0) counts in the row sum alone
+            s[0] = nks * a.scale_log2;
             s[128] = log2f(f);
             s[256] = 1.0f / f;
           }
           pushed(bar(T_FULL + slot), INT8 ? tile : 0u);
         }
-        off = noff;
-        ks = nks;
-        vs = nvs;
       }
     }
     while (np > 0) finish_oldest();
@@ -427,6 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           kv_handoff();       // V of the last key tile landed
           issue_pv(2 * nt - 2, v_prev);
           issue_pv(2 * nt - 1, v_prev);
+          commit(bar(T_OLAST + t), 1);
           commit(bar(T_EMPTY + v_prev), nt - 1 >= no ? 2 : 1);
         }
         n += nj;
@@ -478,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     const uint32_t s_addr = lane_addr + C::s_col(t), o_addr = lane_addr + C::o_col(t);
     uint32_t cc = 0;      // chunks of this query tile so far, over all segments
     uint32_t n = 0;       // key tiles so far
+    uint32_t segs = 0;    // segments of this query tile so far
     const int64_t total = a.T * Hq;
     const bool direct = p.slots == 1;
     while (next_segment(u, sg)) {
@@ -543,9 +590,15 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 #pragma unroll
         for (int e = 0; e < HN; e += 2) {
           const uint64_t y2 = INT8 ? f2add(f2pack(x[e], x[e + 1]), nm2) : f2fma(f2pack(x[e], x[e + 1]), c2, nm2);
-          float y0, y1;
-          f2unpack(y2, y0, y1);
-          const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+          float p0, p1;
+          if (((e >> 1) & 7) < kFmaPairs) {
+            exp2_fma2(y2, p0, p1);
+          } else {
+            float y0, y1;
+            f2unpack(y2, y0, y1);
+            p0 = ex2_approx(y0);
+            p1 = ex2_approx(y1);
+          }
           if (INT8) {
             const float2 iv = *reinterpret_cast<const float2*>(sc + 256 + e);
             acc2[(e >> 1) & 3] = f2fma(f2pack(p0, p1), f2pack(iv.x, iv.y), acc2[(e >> 1) & 3]);
@@ -593,9 +646,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       n += sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
 
       // ---- the row's result: partial (O, m, l), or the output
-      if (nt > 0) {     // one phase at a time: a parity wait tells neighbouring phases apart only
-        mbar_wait(bar(T_ODONE + t), cc & 1, err, abort_flag);
-        mbar_wait(bar(T_ODONE + t), (cc - 1) & 1, err, abort_flag);
+      if (m_used == -INFINITY) l = 0.f;      // a row that saw nothing
+      if (nt > 0) {
+        mbar_wait(bar(T_OLAST + t), segs & 1, err, abort_flag);
+        ++segs;
         tc_fence_after();
         __syncwarp();
       }
