@@ -59,20 +59,39 @@ unsigned int* device_error_word() {
   return g_error_ptr[dev];
 }
 
+static tm_status load_encode() {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_encode == nullptr) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
+    if (e != cudaSuccess || fn == nullptr || q != cudaDriverEntryPointSuccess)
+      return cuda_fail(e != cudaSuccess ? static_cast<int>(e) : -1);
+    g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+  }
+  return TM_OK;
+}
+
+bool encode_tiled_map(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int rank, const int64_t* dims,
+                      const int64_t* strides, const int* box, CUtensorMapSwizzle swz) {
+  if (rank < 1 || rank > 5 || load_encode() != TM_OK) return false;
+  cuuint64_t d[5] = {}, s[4] = {};
+  cuuint32_t b[5] = {}, one[5] = {1u, 1u, 1u, 1u, 1u};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = static_cast<cuuint64_t>(dims[i]);
+    b[i] = static_cast<cuuint32_t>(box[i]);
+    if (i + 1 < rank) s[i] = static_cast<cuuint64_t>(strides[i]);
+  }
+  return g_encode(map, dtype, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, s, b, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 tm_status encode_thd_map(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
                          int elem_bytes, int64_t T, int64_t H, int64_t d, int64_t stride_t,
                          int64_t stride_h, int box_d, int box_rows, CUtensorMapSwizzle swz) {
-  {
-    std::lock_guard<std::mutex> lk(g_mu);
-    if (g_encode == nullptr) {
-      void* fn = nullptr;
-      cudaDriverEntryPointQueryResult q;
-      cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
-      if (e != cudaSuccess || fn == nullptr || q != cudaDriverEntryPointSuccess)
-        return cuda_fail(e != cudaSuccess ? static_cast<int>(e) : -1);
-      g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-    }
-  }
+  const tm_status st = load_encode();
+  if (st != TM_OK) return st;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H),
                         static_cast<cuuint64_t>(T)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride_h * elem_bytes),

@@ -31,6 +31,10 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t ba
   if (p.pre_tile) {
     // equal pieces of the line of key tiles, one for each SM
     const int64_t line = Hkv * pre_rows * pre_units;
+    if (line >= (1ll << 31)) {
+      p.bytes = -1;
+      return p;
+    }
     int64_t c = ceil_div(line, kSmsB200);
     if (c < ceil_div(pre_units, kMostSplits)) c = ceil_div(pre_units, kMostSplits);
     if (c > line) c = line;
@@ -706,6 +710,7 @@ extern "C" tm_status tm_attn_shared_prefix(const tm_tensor* q, const tm_paged_kv
        reinterpret_cast<uintptr_t>(prefix_pages)) & 3u)
     return TM_ERR_INVALID_ARG;
   a.plan = shared_plan(T, static_cast<int32_t>(q->H), cache->H, cache->d, batch, max_seqlen, prefix_len, max_kv_len);
+  if (a.plan.bytes < 0) return TM_ERR_UNSUPPORTED;
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < a.plan.bytes)
     return TM_ERR_INVALID_ARG;
   if (T == 0) return TM_OK;

@@ -9,13 +9,13 @@
 // memory over the whole range; a row's reference maximum is raised (and O
 // rescaled) only when a score exceeds it by 2^kLazy.
 //
-// Loads: four warps copy rows of 16-byte pieces (cp.async) from wherever the
-// block table puts them straight into the 128-byte-swizzled layout that the
-// MMAs read; rows past the range are filled with zeros and never read from
-// memory, so pages of any size and strides need no special cases.  A ring of
-// 128 KB keeps two key tiles in flight.
+// Loads: one warp brings K and V with a TMA copy for each page (or 128 slots of
+// it) into the 128-byte-swizzled layout that the MMAs read, through a ring of
+// 128 KB.  A tile that the range ends in, or with a page that cannot be used,
+// is copied row by row (cp.async) instead, the rows past the end as zeros, so
+// that nothing behind a sequence's end is ever used.
 //
-// INT8 pages: the copies bring the codes, which the same warps turn into fp16
+// INT8 pages: the copies bring the codes, which four more warps turn into fp16
 // in place (exactly).  The scales never touch the codes: with t_j = s_j ks_j +
 // log2 vs_j the weights 2^(t_j - m) of the P.V product carry the V scale, and
 // the row sum takes 2^(t_j - m) / vs_j; both cost no more than scaling the
@@ -36,7 +36,6 @@
 namespace tmk {
 namespace {
 
-constexpr int kThreads = 512;
 // 2^kPOffset is the largest weight when the reference is the maximum; scores
 // up to 2^kLazy above it are left alone: 2^15 at most, inside fp16.
 constexpr float kLazy = 15.0f - kPOffset;
@@ -48,7 +47,7 @@ constexpr float kLazy = 15.0f - kPOffset;
 #endif
 constexpr int kFmaPairs = TM_FMA_PAIRS;
 
-template <int D>
+template <int D, bool INT8>
 struct CfgT {
   static constexpr int BM = 128, BN = 128;
   static constexpr int HALF = 128 * 128;               // one 64-column slab of a tile
@@ -62,9 +61,13 @@ struct CfgT {
   static constexpr int SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t IDESC_S = idesc_f16(BM, 64, false);
   static constexpr uint32_t IDESC_PV = idesc_f16(BM, D, true);
-  // registers: 512 x 128 at launch; 2 x 128 x 200 + 256 x 56 after the split
-  static constexpr int SOFTMAX_REGS = 200, OTHER_REGS = 56;
-  static_assert(2 * 128 * SOFTMAX_REGS + 256 * OTHER_REGS == 512 * 128, "register split");
+  static constexpr int CODES = BN * D;                 // INT8: a K or V tile's codes, in the slot's upper half
+  static constexpr int LOADED = INT8 ? CODES : SLOT;   // bytes that a tile's copies bring
+  // Registers at launch, and after the split over softmax, control and (INT8) conversion warpgroups.
+  static constexpr int THREADS = INT8 ? 512 : 384, LAUNCH_REGS = INT8 ? 128 : 168;
+  static constexpr int SOFTMAX_REGS = INT8 ? 200 : 216, CONTROL_REGS = INT8 ? 56 : 72, CONVERT_REGS = INT8 ? 56 : 0;
+  static_assert(2 * 128 * SOFTMAX_REGS + 128 * CONTROL_REGS + 128 * CONVERT_REGS == THREADS * LAUNCH_REGS,
+                "register split");
   static_assert(SMEM <= 232448, "shared memory per CTA");
   __host__ __device__ static constexpr uint32_t s_col(int t) { return 128u * t; }
   __host__ __device__ static constexpr uint32_t o_col(int t) { return 256u + D * t; }
@@ -79,18 +82,21 @@ enum {
   T_FULL = 10,    // +NSLOT
   T_EMPTY = 18,   // +NSLOT
   T_OLAST = 26,   // +2: a segment's last P.V (T_ODONE's parity cannot tell it from the one two before)
-  T_COUNT = 28
+  T_CODES = 28,   // +NSLOT: INT8, a tile's codes landed
+  T_COUNT = 36
 };
 // Named barriers: NB_P + t softmax t -> issuer t (P stored); NB_KV + t wait
-// helper -> issuer t (operands landed); NB_START softmax A -> issuer B.
-enum : int { NB_P = 1, NB_KV = 3, NB_START = 5 };
+// helper -> issuer t (operands landed); NB_START softmax A -> issuer B; NB_CVT the
+// conversion warps.
+enum : int { NB_P = 1, NB_KV = 3, NB_START = 5, NB_CVT = 6 };
 
-// One row block against one range of keys.
+// One row block against one range of keys (packed rows, keys and key tiles of
+// the line all stay below 2^31).
 struct Segment {
   int kvh, b, slot, rows;     // rows of the block: 1 .. 256
-  int64_t row0, start;        // first packed row (of the batch or the sequence), first token
-  int64_t key0, lk;           // first key, keys that exist
-  int64_t hidden;             // own, causal: token i of the sequence sees keys below hidden + i
+  int row0, start;            // first packed row (of the batch or the sequence), first token
+  int key0, lk;               // first key, keys that exist
+  int hidden;                 // own, causal: token i of the sequence sees keys below hidden + i
   int nj[2];                  // key tiles that each query tile sees
 };
 
@@ -117,10 +123,17 @@ __device__ __forceinline__ void exp2_fma2(uint64_t y2, float& p0, float& p1) {
   p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
 }
 
+struct TileMaps {
+  CUtensorMap q, k, v;
+  int q_tma;          // Q through its map: 128 rows are whole tokens
+  int kv_tma;         // K and V through theirs
+  int heads_inner;    // order of the page maps' middle dimensions: (heads, slots) or (slots, heads)
+};
+
 template <int D, bool INT8>
-__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ SharedArgs a, int prefix,
-                                                           DevErr err) {
-  using C = CfgT<D>;
+__global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
+    tile_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ TileMaps maps, int prefix, DevErr err) {
+  using C = CfgT<D, INT8>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw_s & 1023u)) & 1023u;
@@ -137,77 +150,70 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   pdl_launch_dependents();
 
   // ---- this CTA's segments, walked by every role alike
-  int64_t unit = 0, unit_end = 1;         // prefix: key tiles of the line
+  int unit = 0, unit_end = 1;         // prefix: key tiles of the line
   if (prefix) {
-    unit = static_cast<int64_t>(blockIdx.x) * p.pre_chunk;
-    const int64_t line = static_cast<int64_t>(H) * p.pre_rows * p.pre_tiles;
-    unit_end = unit + p.pre_chunk < line ? unit + p.pre_chunk : line;
+    unit = blockIdx.x * p.pre_chunk;
+    const int line = H * p.pre_rows * p.pre_tiles;
+    unit_end = p.pre_chunk < line - unit ? unit + p.pre_chunk : line;
   }
-  auto next_segment = [&](int64_t& u, Segment& s) -> bool {
+  auto next_segment = [&](int& u, Segment& s) -> bool {
     if (u >= unit_end) return false;
-    s.b = 0;
-    s.start = s.hidden = 0;
-    s.nj[0] = s.nj[1] = 0;
+    s.b = s.start = s.hidden = s.nj[0] = s.nj[1] = 0;
     if (prefix) {
-      const int64_t rb = u / p.pre_tiles;
-      const int64_t first = u - rb * p.pre_tiles;
-      int64_t count = p.pre_tiles - first;
-      if (count > unit_end - u) count = unit_end - u;
+      const int rb = u / p.pre_tiles;
+      const int first = u - rb * p.pre_tiles;
+      const int count = min(p.pre_tiles - first, unit_end - u);
+      s.slot = static_cast<int>(blockIdx.x) - (u - first) / p.pre_chunk;
       u += count;
-      s.kvh = static_cast<int>(rb / p.pre_rows);
-      s.row0 = (rb - static_cast<int64_t>(s.kvh) * p.pre_rows) * 256;
-      s.slot = static_cast<int>(blockIdx.x - rb * p.pre_tiles / p.pre_chunk);
+      s.kvh = rb / p.pre_rows;
+      s.row0 = (rb - s.kvh * p.pre_rows) * 256;
       s.key0 = first * 128;
-      s.lk = a.prefix_len;
-      const int64_t n = rows_in_use(a) * g - s.row0;
-      s.rows = n < 0 ? 0 : (n < 256 ? static_cast<int>(n) : 256);
-      if (s.rows > 0) s.nj[0] = static_cast<int>(count);
-      if (s.rows > 128) s.nj[1] = static_cast<int>(count);
+      s.lk = static_cast<int>(a.prefix_len);
+      s.rows = max(0, min(static_cast<int>(rows_in_use(a)) * g - s.row0, 256));
+      if (s.rows > 0) s.nj[0] = count;
+      if (s.rows > 128) s.nj[1] = count;
       return true;
     }
     u = unit_end;
-    int64_t item = blockIdx.x;
-    s.kvh = static_cast<int>(item % H);
+    int item = blockIdx.x;
+    s.kvh = item % H;
     item /= H;
-    const int64_t per = static_cast<int64_t>(a.batch) * p.own_rows;
-    const int split = static_cast<int>(item / per);
-    item %= per;
-    s.b = static_cast<int>(item / p.own_rows);
-    s.row0 = (item % p.own_rows) * 256;
+    const int per = a.batch * p.own_rows;
+    const int split = item / per;
+    item -= split * per;
+    s.b = item / p.own_rows;
+    s.row0 = (item - s.b * p.own_rows) * 256;
     s.slot = p.pre_splits + split;
-    s.key0 = static_cast<int64_t>(split) * p.own_chunk;
-    int64_t n;
-    seq_rows(a, s.b, s.start, n);
+    s.key0 = split * p.own_chunk;
     s.rows = 0;
-    const bool outside = s.start < 0 || n < 0 || s.start + n > a.T || n * g > static_cast<int64_t>(p.own_rows) * 256;
+    int64_t start, n64;
+    seq_rows(a, s.b, start, n64);
+    const bool outside = start < 0 || n64 < 0 || start + n64 > a.T || n64 * g > static_cast<int64_t>(p.own_rows) * 256;
     if (outside && threadIdx.x == 0) dev_error(err, TM_DEVERR_SEQLEN);
+    const int n = static_cast<int>(n64);
     if (outside || s.row0 >= n * g) return true;
-    s.rows = static_cast<int>(n * g - s.row0 < 256 ? n * g - s.row0 : 256);
-    s.lk = __ldg(a.kv_lens + s.b);
-    if (s.lk > a.max_kv) {
+    s.start = static_cast<int>(start);
+    s.rows = min(n * g - s.row0, 256);
+    int lk = __ldg(a.kv_lens + s.b);
+    if (lk > a.max_kv) {
       if (threadIdx.x == 0) dev_error(err, TM_DEVERR_SEQLEN);
-      s.lk = a.max_kv;
+      lk = static_cast<int>(a.max_kv);
     }
-    s.hidden = s.lk - n + 1;
-    int64_t end = s.key0 + p.own_chunk < s.lk ? s.key0 + p.own_chunk : s.lk;
+    s.hidden = lk - n + 1;
+    s.lk = max(0, min(s.key0 + p.own_chunk, lk));
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (s.rows <= 128 * t) continue;
-      int64_t seen = end;
-      if (a.causal) {
-        const int64_t last = s.row0 + (s.rows < 128 * (t + 1) ? s.rows : 128 * (t + 1)) - 1;
-        const int64_t l = s.hidden + last / g;
-        if (l < seen) seen = l;
-      }
-      s.nj[t] = seen > s.key0 ? static_cast<int>((seen - s.key0 + 127) / 128) : 0;
+      int seen = s.lk;
+      if (a.causal) seen = min(seen, s.hidden + (s.row0 + min(s.rows, 128 * (t + 1)) - 1) / g);
+      s.nj[t] = seen > s.key0 ? (seen - s.key0 + 127) / 128 : 0;
     }
-    s.lk = end > 0 ? end : 0;
     return true;
   };
 
   // ---- setup
   if (threadIdx.x == 0) {
-    mbar_init(bar(T_QFULL), 4);
+    mbar_init(bar(T_QFULL), 1);
     mbar_init(bar(T_QEMPTY), 2);
     for (int i = 0; i < 4; ++i) mbar_init(bar(T_SFULL + i), 1);
     for (int t = 0; t < 2; ++t) {
@@ -216,8 +222,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       mbar_init(bar(T_OLAST + t), 1);
     }
     for (int s = 0; s < C::NSLOT; ++s) {
-      mbar_init(bar(T_FULL + s), 4);
+      mbar_init(bar(T_FULL + s), INT8 ? 4 : 1);
       mbar_init(bar(T_EMPTY + s), 2);
+      if (INT8) mbar_init(bar(T_CODES + s), 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -230,172 +237,208 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int64_t u = unit;
+  int u = unit;
   Segment sg;
 
-  if (warp >= 12) {
-    // ======================= loaders (warp w: rows 32 w .. of each tile) ====
-    regs_dec<C::OTHER_REGS>();
-    const int w = warp - 12;
-    const int shift = a.pool.page_shift;
-    const int64_t page_mask = (1ll << shift) - 1;
-    constexpr int ROW = D * (INT8 ? 1 : 2), PIECES = ROW / 16, RPI = 32 / PIECES;
-    constexpr int CODE_OFF = INT8 && D == 128 ? C::HALF : 0;   // codes wait inside their own row's fp16 place
-    // up to three groups of copies in flight, oldest first: barrier to signal and (INT8) the tile to convert
-    uint32_t pb0 = 0, pb1 = 0, pb2 = 0, pt0 = 0, pt1 = 0, pt2 = 0;
-    int np = 0;
-    auto finish_oldest = [&]() {
-      if (np == 3) cp_wait<2>();
-      else if (np == 2) cp_wait<1>();
-      else cp_wait<0>();
-      __syncwarp();
-      if (INT8 && pt0 != 0) {
-        const int r = 32 * w + lane;
-        const uint32_t row = pt0 + r * 128;
-#pragma unroll
-        for (int half = 0; half < D / 64; ++half) {
-          uint4 c[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) c[i] = lds128(row + CODE_OFF + (((4 * half + i) ^ (r & 7)) << 4));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t x[4] = {c[i].x ^ 0x80808080u, c[i].y ^ 0x80808080u, c[i].z ^ 0x80808080u,
-                                   c[i].w ^ 0x80808080u};
-            const uint32_t at = row + half * C::HALF;
-            sts128(at + (((2 * i) ^ (r & 7)) << 4), make_uint4(codes2(x[0], 0x4140u), codes2(x[0], 0x4342u),
-                                                               codes2(x[1], 0x4140u), codes2(x[1], 0x4342u)));
-            sts128(at + (((2 * i + 1) ^ (r & 7)) << 4), make_uint4(codes2(x[2], 0x4140u), codes2(x[2], 0x4342u),
-                                                                   codes2(x[3], 0x4140u), codes2(x[3], 0x4342u)));
-          }
-        }
-      }
-      fence_async_shared();    // these stores are read by tcgen05.mma
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pb0);
-      pb0 = pb1;
-      pb1 = pb2;
-      pt0 = pt1;
-      pt1 = pt2;
-      --np;
-    };
-    // Waits for a barrier; groups that have not been signalled yet come first when it is not free.
-    auto acquire = [&](uint32_t b, uint32_t parity) {
-      if (np == 3) finish_oldest();
-      while (np > 0 && !__shfl_sync(0xffffffffu, static_cast<int>(mbar_test_wait(b, parity)), 0)) finish_oldest();
-      mbar_wait_warp(b, parity, err, abort_flag);
-    };
-    auto pushed = [&](uint32_t b, uint32_t tile) {
-      cp_commit();
-      if (np == 0) { pb0 = b; pt0 = tile; }
-      else if (np == 1) { pb1 = b; pt1 = tile; }
-      else { pb2 = b; pt2 = tile; }
-      ++np;
-    };
-    uint32_t n = 0, qn = 0;
-    const int64_t st = a.pool.stride_t;
-    const int c = lane % PIECES, sub = lane / PIECES;
+  // Page of key `key` of a segment: -1 behind its end, -2 where it cannot be used
+  const int shift = a.pool.page_shift;
+  const int page_mask = (1 << shift) - 1;
+  auto page_at = [&](const Segment& s, int key) -> int32_t {
+    if (key >= s.lk) return -1;
+    const int col = key >> shift;
+    int32_t page;
+    if (prefix) page = __ldg(a.prefix_pages + col);
+    else page = col < a.pt.cols ? __ldg(a.pt.table + s.b * a.pt.stride + col) : -1;
+    return page_ok(page, a.pool.num_pages) ? page : -2;
+  };
+
+  if (INT8 && warp >= 12) {
+    // ======================= conversion of codes (thread r: key row r of each tile) ====
+    regs_dec<C::CONVERT_REGS>();
+    const int r = threadIdx.x - 384;
+    uint32_t n = 0;
     while (next_segment(u, sg)) {
       const int nj = sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
-      if (nj == 0) continue;
-      const uint8_t* kbase = a.pool.k + sg.kvh * a.pool.stride_h + c * 16;
-      const uint8_t* vbase = a.pool.v + sg.kvh * a.pool.stride_h + c * 16;
-      const int64_t first = sg.key0 + 32 * w;        // this warp's first key of tile 0
-      // Pages of this warp's two runs of 16 keys of key tile j (a run never crosses a page), -1 where there is
-      // nothing to read.  Loaded one tile ahead.
-      auto page_at = [&](int j, int run) -> int32_t {
-        const int64_t key = first + static_cast<int64_t>(j) * 128 + 16 * run;
-        if (j >= nj || key >= sg.lk) return -1;
-        const int64_t col = key >> shift;
-        if (prefix) return __ldg(a.prefix_pages + col);
-        return col < a.pt.cols ? __ldg(a.pt.table + sg.b * a.pt.stride + col) : -2;
+      auto scales_of = [&](int j, float& ks, float& vs) {
+        const int key = sg.key0 + j * 128 + r;
+        const int32_t page = j < nj ? page_at(sg, key) : -1;
+        ks = vs = 0.f;
+        if (page < 0) return;
+        const int64_t so = page * a.pool.sstride_page + (key & page_mask) * a.pool.sstride_t + sg.kvh * a.pool.sstride_h;
+        ks = __half2float(a.pool.ks[so]);
+        vs = __half2float(a.pool.vs[so]);
       };
-      // Copies this warp's rows of one tile; base[run]: the run's first row, valid[run]: its rows to read
-      auto copy_rows = [&](uint32_t tile, const uint8_t* base, const int64_t (&off)[2], const int (&valid)[2]) {
-#pragma unroll
-        for (int run = 0; run < 2; ++run) {
-          const uint8_t* src = base + off[run];
-#pragma unroll
-          for (int i = 0; i < 16 / RPI; ++i) {
-            const int rr = i * RPI + sub;
-            const int r = 32 * w + 16 * run + rr;
-            const uint32_t dst = tile + (INT8 ? CODE_OFF : (c >> 3) * C::HALF) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-            const bool real = rr < valid[run];
-            cp16(dst, real ? src + rr * st : base, real);
-          }
-        }
-      };
-      int32_t page[2] = {page_at(0, 0), page_at(0, 1)};
-      // Q of both tiles, once the MMAs of the last segment have read theirs
-      if (np == 3) finish_oldest();
-      if (qn > 0) acquire(bar(T_QEMPTY), (qn - 1) & 1);
-      ++qn;
-      {
-        constexpr int QP = D / 8;
-        const int qc = lane % QP;
-        const uint32_t row0 = static_cast<uint32_t>(sg.row0), gg = static_cast<uint32_t>(g);
-        const __half* qbase = a.q + sg.start * a.q_t + static_cast<int64_t>(sg.kvh) * g * a.q_h + qc * 8;
-#pragma unroll 4
-        for (int i = 0; i < 2 * QP; ++i) {      // 64 rows of this warp, 32 / QP at a time
-          const int k = i * (32 / QP) + lane / QP;
-          const int t = k >> 5, r = 32 * w + (k & 31);
-          const int pr = 128 * t + r;
-          const bool real = pr < sg.rows;
-          const uint32_t row = row0 + pr, tok = row / gg;
-          const __half* src = real ? qbase + tok * a.q_t + (row - tok * gg) * a.q_h : a.q;
-          cp16(sbase + t * C::Q_BYTES + (qc >> 3) * C::HALF + r * 128 + (((qc & 7) ^ (r & 7)) << 4), src, real);
-        }
-        pushed(bar(T_QFULL), 0);
-      }
-      float nks = 0.f, nvs = 0.f;      // INT8: scales of this lane's key, loaded while K is copied
+      float ks, vs, ks_next, vs_next;
+      scales_of(0, ks_next, vs_next);
       for (int j = 0; j < nj; ++j, ++n) {
-        int64_t off[2];
-        int valid[2];
-#pragma unroll
-        for (int run = 0; run < 2; ++run) {
-          const int64_t key = first + static_cast<int64_t>(j) * 128 + 16 * run;
-          const int64_t left = sg.lk - key;
-          bool use = left > 0;
-          if (use && !page_ok(page[run], a.pool.num_pages)) {
-            if (lane == 0) dev_error(err, TM_DEVERR_SEQLEN);
-            use = false;
-          }
-          valid[run] = use ? (left < 16 ? static_cast<int>(left) : 16) : 0;
-          off[run] = use ? page[run] * a.pool.stride_page + (key & page_mask) * a.pool.stride_t : 0;
-        }
-        if (INT8) {
-          const int run = lane >> 4;
-          const int64_t key = first + static_cast<int64_t>(j) * 128 + lane;
-          nks = nvs = 0.f;
-          if ((lane & 15) < valid[run]) {
-            const int64_t so = page[run] * a.pool.sstride_page + (key & page_mask) * a.pool.sstride_t +
-                               sg.kvh * a.pool.sstride_h;
-            nks = __half2float(a.pool.ks[so]);
-            nvs = __half2float(a.pool.vs[so]);
-          }
-        }
-        page[0] = page_at(j + 1, 0);
-        page[1] = page_at(j + 1, 1);
-#pragma unroll
+        ks = ks_next;
+        vs = vs_next;
+        scales_of(j + 1, ks_next, vs_next);
+#pragma unroll 1
         for (int v = 0; v < 2; ++v) {
-          const uint32_t i = 2 * n + v, slot = i % C::NSLOT, lap = i / C::NSLOT;
-          if (lap > 0) acquire(bar(T_EMPTY + slot), (lap - 1) & 1);
-          else if (np == 3) finish_oldest();
+          const uint32_t i = 2 * n + v, slot = i % C::NSLOT;
+          mbar_wait_warp(bar(T_CODES + slot), (i / C::NSLOT) & 1, err, abort_flag);
           const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT;
-          copy_rows(tile, v ? vbase : kbase, off, valid);
-          if (INT8 && v) {      // the V tile's release frees its stage of scales
-            float* s = scales + (slot >> 1) * 384 + 32 * w + lane;
-            const float f = nvs == 0.f ? 5.9604645e-8f : nvs;   // a zero scale (codes all 0) counts in the row sum alone
-            s[0] = nks * a.scale_log2;
+          if (v) {      // the V tile's release frees its stage of scales
+            float* s = scales + (slot >> 1) * 384 + r;
+            const float f = vs == 0.f ? 5.9604645e-8f : vs;   // a zero scale (codes all 0) counts in the row sum alone
+            s[0] = ks * a.scale_log2;
             s[128] = log2f(f);
             s[256] = 1.0f / f;
           }
-          pushed(bar(T_FULL + slot), INT8 ? tile : 0u);
+          // d = 128: the codes lie where the upper 64 columns go, row r's in row r's place, and are read before
+          // that is written.  d = 64: 64-byte rows over other rows' places, so all are read first.
+#pragma unroll
+          for (int half = 0; half < D / 64; ++half) {
+            const uint32_t src = D == 128 ? tile + C::HALF + r * 128 : tile + C::CODES + r * 64;
+            const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
+            uint4 c[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) c[q] = lds128(src + (((4 * half + q) ^ sw) << 4));
+            if (D == 64) named_bar_sync(NB_CVT, 128);
+            const uint32_t at = tile + half * C::HALF + r * 128;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t x[4] = {c[q].x ^ 0x80808080u, c[q].y ^ 0x80808080u, c[q].z ^ 0x80808080u,
+                                     c[q].w ^ 0x80808080u};
+              sts128(at + (((2 * q) ^ (r & 7)) << 4), make_uint4(codes2(x[0], 0x4140u), codes2(x[0], 0x4342u),
+                                                                 codes2(x[1], 0x4140u), codes2(x[1], 0x4342u)));
+              sts128(at + (((2 * q + 1) ^ (r & 7)) << 4), make_uint4(codes2(x[2], 0x4140u), codes2(x[2], 0x4342u),
+                                                                     codes2(x[3], 0x4140u), codes2(x[3], 0x4342u)));
+            }
+          }
+          fence_async_shared();    // read by tcgen05.mma
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(T_FULL + slot));
         }
       }
     }
-    while (np > 0) finish_oldest();
   } else if (warp >= 8) {
-    regs_dec<C::OTHER_REGS>();
+    regs_dec<C::CONTROL_REGS>();
+    if (warp == 8) {
+      // ======================= loader =======================
+      uint32_t n = 0, qn = 0;
+      const int box_shift = shift < 7 ? shift : 7;       // key rows of a copy
+      const int boxes = 128 >> box_shift;
+      const int LANDED = INT8 ? T_CODES : T_FULL;
+      constexpr uint32_t DST = INT8 ? C::SLOT / 2 : 0;
+      // a whole tile: lane i copies box i, whose page it holds
+      auto copy_boxes = [&](const CUtensorMap* map, uint32_t slot, int32_t page, int key) {
+        const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT + DST;
+        if (lane == 0) mbar_arrive_expect_tx(bar(LANDED + slot), C::LOADED);
+        __syncwarp();
+        if (lane < boxes) {
+          const int32_t s0 = key & page_mask;
+          const int32_t c1 = maps.heads_inner ? sg.kvh : s0, c2 = maps.heads_inner ? s0 : sg.kvh;
+#pragma unroll
+          for (int hh = 0; hh < (INT8 ? 1 : D / 64); ++hh)
+            tma_load_4d(tile + hh * C::HALF + (lane << box_shift) * (INT8 ? D : 128), map, bar(LANDED + slot), hh * 64,
+                        c1, c2, page);
+        }
+        __syncwarp();
+      };
+      // a ragged tile: row by row; the page of each run of 16 keys is in lane `run`
+      auto copy_rows = [&](const uint8_t* base, uint32_t slot, int32_t page, int key0) {
+        constexpr int ROW = D * (INT8 ? 1 : 2), PIECES = ROW / 16, RPI = 32 / PIECES;
+        const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT + DST;
+        const int c = lane % PIECES;
+#pragma unroll 1
+        for (int run = 0; run < 8; ++run) {
+          const int32_t pg = __shfl_sync(0xffffffffu, page, run);
+          const int key = key0 + 16 * run;
+          const uint8_t* src = base + c * 16 + (pg >= 0 ? pg * a.pool.stride_page + (key & page_mask) * a.pool.stride_t : 0);
+#pragma unroll
+          for (int i = 0; i < 16 / RPI; ++i) {
+            const int rr = i * RPI + lane / PIECES;
+            const int r = 16 * run + rr;
+            const uint32_t dst = INT8 && D == 64 ? tile + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)
+                                                 : tile + (c >> 3) * C::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            const bool real = pg >= 0 && key + rr < sg.lk;
+            cp16(dst, real ? src + rr * a.pool.stride_t : base, real);
+          }
+        }
+        cp_commit();
+      };
+      auto acquire = [&](uint32_t i) {
+        if (i >= C::NSLOT) mbar_wait_warp(bar(T_EMPTY + i % C::NSLOT), (i / C::NSLOT - 1) & 1, err, abort_flag);
+      };
+      auto landed = [&](uint32_t b) {
+        fence_async_shared();      // read by tcgen05.mma
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b);
+      };
+      while (next_segment(u, sg)) {
+        const int nj = sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
+        if (nj == 0) continue;
+        // Q of both tiles, once the MMAs of the last segment have read theirs
+        if (qn > 0) mbar_wait_warp(bar(T_QEMPTY), (qn - 1) & 1, err, abort_flag);
+        ++qn;
+        const uint32_t gg = static_cast<uint32_t>(g);
+        if (maps.q_tma) {
+          if (lane == 0) mbar_arrive_expect_tx(bar(T_QFULL), 2 * C::Q_BYTES);
+          __syncwarp();
+          if (lane < 2 * (D / 64)) {
+            const int t = lane & 1, hh = lane >> 1;
+            const int32_t token = sg.start + (sg.row0 + 128 * t) / g;
+            tma_load_3d(sbase + t * C::Q_BYTES + hh * C::HALF, &maps.q, bar(T_QFULL), hh * 64, sg.kvh * g, token);
+          }
+          __syncwarp();
+        } else {
+          constexpr int QP = D / 8;
+          const int qc = lane % QP;
+          const uint32_t row0 = static_cast<uint32_t>(sg.row0);
+          const __half* qbase = a.q + static_cast<int64_t>(sg.start) * a.q_t + static_cast<int64_t>(sg.kvh) * g * a.q_h + qc * 8;
+#pragma unroll 4
+          for (int i = 0; i < 8 * QP; ++i) {
+            const int pr = i * (32 / QP) + lane / QP;
+            const bool real = pr < sg.rows;
+            const uint32_t row = row0 + pr, tok = row / gg;
+            const __half* src = real ? qbase + tok * a.q_t + (row - tok * gg) * a.q_h : a.q;
+            const int r = pr & 127;
+            cp16(sbase + (pr >> 7) * C::Q_BYTES + (qc >> 3) * C::HALF + r * 128 + (((qc & 7) ^ (r & 7)) << 4), src, real);
+          }
+          cp_commit();
+          cp_wait<0>();
+          landed(bar(T_QFULL));
+        }
+        // lanes 0-7: pages of the 16-key runs (box i's page is in lane i of page_of_box)
+        const int step = 128 / boxes;
+        auto my_page = [&](int j) -> int32_t {
+          const int key = sg.key0 + j * 128 + lane * step;
+          return j < nj && lane < boxes ? page_at(sg, key) : -1;
+        };
+        int32_t page = my_page(0);
+        for (int j = 0; j < nj; ++j, ++n) {
+          const int key0 = sg.key0 + j * 128;
+          const int32_t next = my_page(j + 1);
+          if (page == -2) dev_error(err, TM_DEVERR_SEQLEN);
+          const uint32_t i = 2 * n;
+          if (maps.kv_tma && key0 + 128 <= sg.lk && __all_sync(0xffffffffu, lane >= boxes || page >= 0)) {
+            const int key = key0 + lane * step;
+            acquire(i);
+            copy_boxes(&maps.k, i % C::NSLOT, page, key);
+            acquire(i + 1);
+            copy_boxes(&maps.v, (i + 1) % C::NSLOT, page, key);
+          } else {
+            const int32_t run_page = __shfl_sync(0xffffffffu, page, ((lane & 7) * 16) >> box_shift);
+            acquire(i);
+            copy_rows(a.pool.k + sg.kvh * a.pool.stride_h, i % C::NSLOT, run_page, key0);
+            acquire(i + 1);
+            copy_rows(a.pool.v + sg.kvh * a.pool.stride_h, (i + 1) % C::NSLOT, run_page, key0);
+            cp_wait<1>();
+            landed(bar(LANDED + i % C::NSLOT));
+            cp_wait<0>();
+            landed(bar(LANDED + (i + 1) % C::NSLOT));
+          }
+          page = next;
+        }
+      }
+      // every copy has landed before the block may end
+      volatile int never = 0;
+      if (qn > 0) mbar_wait_warp(bar(T_QFULL), (qn - 1) & 1, err, &never);
+      for (uint32_t i = 2 * n > C::NSLOT ? 2 * n - C::NSLOT : 0; i < 2 * n; ++i)
+        mbar_wait_warp(bar(LANDED + i % C::NSLOT), (i / C::NSLOT) & 1, err, &never);
+    }
     if (warp == 9 || warp == 10) {
       // ======================= tcgen05 issuers (warp 9: tile A, warp 10: tile B) ====
       // They never touch shared memory: the wait helper polls for them.
@@ -531,14 +574,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       const int nt = sg.nj[t];
       const int pr = 128 * t + r;
       const bool row_ok = pr < sg.rows;
-      const int64_t prow = sg.row0 + pr;
-      const int64_t tok_in = prow / g;
-      const int64_t tok = sg.start + tok_in;
-      const int head = sg.kvh * g + static_cast<int>(prow - tok_in * g);
-      int64_t lim = 0;
+      const int prow = sg.row0 + pr, tok_in = prow / g;
+      const int tok = sg.start + tok_in, head = sg.kvh * g + prow - tok_in * g;
+      int lim = 0;
       if (row_ok) {
         lim = sg.lk;
-        if (!prefix && a.causal && sg.hidden + tok_in < lim) lim = sg.hidden + tok_in;
+        if (!prefix && a.causal) lim = min(lim, sg.hidden + tok_in);
       }
       float m_used = -INFINITY, l = 0.f;
       for (int c = 0; c < 2 * nt; ++c, ++cc) {
@@ -569,8 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           }
         }
         const float cs = INT8 ? 1.0f : a.scale_log2;
-        const int64_t nv64 = lim - (sg.key0 + static_cast<int64_t>(c) * HN);
-        const int nv = nv64 <= 0 ? 0 : (nv64 >= HN ? HN : static_cast<int>(nv64));
+        const int nv = max(0, min(lim - sg.key0 - c * HN, HN));
         if (!__all_sync(0xffffffffu, nv == HN)) {
 #pragma unroll
           for (int e = 0; e < HN; ++e) x[e] = (e < nv) ? x[e] : -INFINITY;
@@ -653,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         tc_fence_after();
         __syncwarp();
       }
-      const int64_t idx = sg.slot * total + tok * Hq + head;
+      const int64_t idx = sg.slot * total + static_cast<int64_t>(tok) * Hq + head;
       if (row_ok && !direct) a.ml[idx] = make_float2(m_used, l);
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
       if (nt > 0 || direct) {
@@ -702,13 +742,37 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 
 template <int D, bool INT8>
 static tm_status launch_tile(const SharedArgs& a, bool prefix, bool overlap, DevErr err, cudaStream_t stream) {
-  constexpr int smem = CfgT<D>::SMEM;
+  using C = CfgT<D, INT8>;
   static std::atomic<uint64_t> prepared{0};
-  tm_status st = prepare_smem(tile_kernel<D, INT8>, smem, prepared);
+  tm_status st = prepare_smem(tile_kernel<D, INT8>, C::SMEM, prepared);
   if (st != TM_OK) return st;
   const SharedPlan& p = a.plan;
-  const int64_t items = prefix ? p.pre_ctas : static_cast<int64_t>(p.own_splits) * a.batch * p.own_rows * a.pool.H;
-  return launch_kernel(tile_kernel<D, INT8>, items, kThreads, smem, overlap, stream, a, prefix ? 1 : 0, err);
+  const PagedPool& pool = a.pool;
+  TileMaps m{};
+  const int g = p.group, Hq = pool.H * g;
+  const int64_t box_rows = pool.page_shift < 7 ? 1 << pool.page_shift : 128;
+  // pages as a tensor [page][slot or head][head or slot][d]
+  m.heads_inner = pool.stride_h < pool.stride_t;
+  const int64_t page_size = 1ll << pool.page_shift;
+  const int64_t dims[4] = {D, m.heads_inner ? pool.H : page_size, m.heads_inner ? page_size : pool.H, pool.num_pages};
+  const int64_t strides[3] = {m.heads_inner ? pool.stride_h : pool.stride_t, m.heads_inner ? pool.stride_t : pool.stride_h,
+                              pool.stride_page};
+  const int box[4] = {INT8 ? D : 64, static_cast<int>(m.heads_inner ? 1 : box_rows),
+                      static_cast<int>(m.heads_inner ? box_rows : 1), 1};
+  const CUtensorMapDataType type = INT8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUtensorMapSwizzle swz = INT8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  // where the driver has no map for a layout, rows are copied one by one
+  m.kv_tma = encode_tiled_map(&m.k, pool.k, type, 4, dims, strides, box, swz) &&
+             encode_tiled_map(&m.v, pool.v, type, 4, dims, strides, box, swz);
+  if (128 % g == 0) {
+    const int64_t qdims[3] = {D, Hq, a.T};
+    const int64_t qstrides[2] = {(Hq > 1 ? a.q_h : D) * 2, (a.T > 1 ? a.q_t : D * Hq) * 2};
+    const int qbox[3] = {64, g, 128 / g};
+    m.q_tma = encode_tiled_map(&m.q, a.q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, qdims, qstrides, qbox,
+                               CU_TENSOR_MAP_SWIZZLE_128B);
+  }
+  const int64_t items = prefix ? p.pre_ctas : static_cast<int64_t>(p.own_splits) * a.batch * p.own_rows * pool.H;
+  return launch_kernel(tile_kernel<D, INT8>, items, C::THREADS, C::SMEM, overlap, stream, a, m, prefix ? 1 : 0, err);
 }
 
 tm_status shared_tile(const SharedArgs& a, int d, bool int8, bool prefix, bool overlap, DevErr err,

@@ -27,6 +27,11 @@ tm_status encode_thd_map(CUtensorMap* map, const void* base, CUtensorMapDataType
                          int elem_bytes, int64_t T, int64_t H, int64_t d, int64_t stride_t,
                          int64_t stride_h, int box_d, int box_rows, CUtensorMapSwizzle swz);
 
+// cuTensorMapEncodeTiled for any rank (strides in bytes, of dimension 1 on);
+// false where the driver refuses the layout.
+bool encode_tiled_map(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int rank, const int64_t* dims,
+                      const int64_t* strides, const int* box, CUtensorMapSwizzle swz);
+
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 }  // namespace tmk
