@@ -16,10 +16,11 @@
 // that nothing behind a sequence's end is ever used.
 //
 // INT8 pages: the copies bring the codes, which four more warps turn into fp16
-// in place (exactly).  The scales never touch the codes: with t_j = s_j ks_j +
-// log2 vs_j the weights 2^(t_j - m) of the P.V product carry the V scale, and
-// the row sum takes 2^(t_j - m) / vs_j; both cost no more than scaling the
-// scores, and the weights keep fp16's full range whatever the scales are.
+// in place.  K stays codes (exactly) and a key's scale multiplies its scores in
+// fp32; V becomes fp16(code * scale), the value that tm_kv_gather gives: its one
+// rounding is of the size of P's, and carrying V's scale in P instead would take
+// a second pass of 128-byte shared-memory reads through the softmax and fp16's
+// range from the weights.
 //
 // The prefix's work is one line of key tiles (row block by row block) cut into
 // equal pieces, one for each CTA, so that all SMs finish together; a CTA whose
@@ -56,8 +57,8 @@ struct CfgT {
   static constexpr int STAGES = NSLOT / 2;
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int OFF_SLOT = 2 * Q_BYTES;
-  static constexpr int OFF_SCALE = OFF_SLOT + NSLOT * SLOT;       // [STAGES][3][128] floats
-  static constexpr int OFF_BAR = OFF_SCALE + STAGES * 3 * 128 * 4;
+  static constexpr int OFF_SCALE = OFF_SLOT + NSLOT * SLOT;       // [STAGES][128] K scales
+  static constexpr int OFF_BAR = OFF_SCALE + STAGES * 128 * 4;
   static constexpr int SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t IDESC_S = idesc_f16(BM, 64, false);
   static constexpr uint32_t IDESC_PV = idesc_f16(BM, D, true);
@@ -85,10 +86,10 @@ enum {
   T_CODES = 28,   // +NSLOT: INT8, a tile's codes landed
   T_COUNT = 36
 };
-// Named barriers: NB_P + t softmax t -> issuer t (P stored); NB_KV + t wait
-// helper -> issuer t (operands landed); NB_START softmax A -> issuer B; NB_CVT the
-// conversion warps.
-enum : int { NB_P = 1, NB_KV = 3, NB_START = 5, NB_CVT = 6 };
+// Named barriers: NB_P + 2 t + half softmax t -> issuer t (P stored); NB_KV + t
+// wait helper -> issuer t (operands landed); NB_TURN + t the other softmax ->
+// softmax t (its turn); NB_CVT the conversion warps.
+enum : int { NB_P = 1, NB_KV = 5, NB_TURN = 7, NB_CVT = 9 };
 
 // One row block against one range of keys (packed rows, keys and key tiles of
 // the line all stay below 2^31).
@@ -129,6 +130,13 @@ struct TileMaps {
   int kv_tma;         // K and V through theirs
   int heads_inner;    // order of the page maps' middle dimensions: (heads, slots) or (slots, heads)
 };
+
+// codes2 times a scale: a code and a product's one rounding
+__device__ __forceinline__ uint32_t scaled2(uint32_t w, uint32_t sel, __half2 by) {
+  const uint32_t c = codes2(w, sel);
+  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&c), by);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 template <int D, bool INT8>
 __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
@@ -259,16 +267,18 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
     uint32_t n = 0;
     while (next_segment(u, sg)) {
       const int nj = sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
-      auto scales_of = [&](int j, float& ks, float& vs) {
+      auto scales_of = [&](int j, float& ks, __half& vs) {
         const int key = sg.key0 + j * 128 + r;
         const int32_t page = j < nj ? page_at(sg, key) : -1;
-        ks = vs = 0.f;
+        ks = 0.f;
+        vs = __float2half(0.f);
         if (page < 0) return;
         const int64_t so = page * a.pool.sstride_page + (key & page_mask) * a.pool.sstride_t + sg.kvh * a.pool.sstride_h;
         ks = __half2float(a.pool.ks[so]);
-        vs = __half2float(a.pool.vs[so]);
+        vs = a.pool.vs[so];
       };
-      float ks, vs, ks_next, vs_next;
+      float ks, ks_next;
+      __half vs, vs_next;
       scales_of(0, ks_next, vs_next);
       for (int j = 0; j < nj; ++j, ++n) {
         ks = ks_next;
@@ -279,13 +289,8 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           const uint32_t i = 2 * n + v, slot = i % C::NSLOT;
           mbar_wait_warp(bar(T_CODES + slot), (i / C::NSLOT) & 1, err, abort_flag);
           const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT;
-          if (v) {      // the V tile's release frees its stage of scales
-            float* s = scales + (slot >> 1) * 384 + r;
-            const float f = vs == 0.f ? 5.9604645e-8f : vs;   // a zero scale (codes all 0) counts in the row sum alone
-            s[0] = ks * a.scale_log2;
-            s[128] = log2f(f);
-            s[256] = 1.0f / f;
-          }
+          if (v) scales[(slot >> 1) * 128 + r] = ks;     // the V tile's release frees its stage of scales
+          const __half2 by = __half2half2(v ? vs : __float2half(1.f));
           // d = 128: the codes lie where the upper 64 columns go, row r's in row r's place, and are read before
           // that is written.  d = 64: 64-byte rows over other rows' places, so all are read first.
 #pragma unroll
@@ -301,10 +306,12 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
             for (int q = 0; q < 4; ++q) {
               const uint32_t x[4] = {c[q].x ^ 0x80808080u, c[q].y ^ 0x80808080u, c[q].z ^ 0x80808080u,
                                      c[q].w ^ 0x80808080u};
-              sts128(at + (((2 * q) ^ (r & 7)) << 4), make_uint4(codes2(x[0], 0x4140u), codes2(x[0], 0x4342u),
-                                                                 codes2(x[1], 0x4140u), codes2(x[1], 0x4342u)));
-              sts128(at + (((2 * q + 1) ^ (r & 7)) << 4), make_uint4(codes2(x[2], 0x4140u), codes2(x[2], 0x4342u),
-                                                                     codes2(x[3], 0x4140u), codes2(x[3], 0x4342u)));
+              sts128(at + (((2 * q) ^ (r & 7)) << 4),
+                     make_uint4(scaled2(x[0], 0x4140u, by), scaled2(x[0], 0x4342u, by), scaled2(x[1], 0x4140u, by),
+                                scaled2(x[1], 0x4342u, by)));
+              sts128(at + (((2 * q + 1) ^ (r & 7)) << 4),
+                     make_uint4(scaled2(x[2], 0x4140u, by), scaled2(x[2], 0x4342u, by), scaled2(x[3], 0x4140u, by),
+                                scaled2(x[3], 0x4342u, by)));
             }
           }
           fence_async_shared();    // read by tcgen05.mma
@@ -482,7 +489,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           at[kk] = d_s + 64u * static_cast<uint32_t>(c & 1) + kk * 8;
           bd[kk] = smem_desc(vb + ((c & 1) * 4 + kk) * 2048, C::HALF, 1024, kSwizzle128);
         }
-        named_bar_sync(NB_P + t, 160);      // softmax t stored P_t(c)
+        named_bar_sync(NB_P + 2 * t + (c & 1), 160);      // softmax t stored P_t(c)
         tc_fence_after();
         if (elect_one()) {
           mma_f16_ts_n<4>(d_o, at, bd, C::IDESC_PV, c > 0 ? 1u : 0u);
@@ -501,7 +508,6 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
             const int share = j >= no ? 2 : 1;           // also the other tile's release where it has no tile j
             kv_handoff();     // K of j (and V of j - 1) landed
             if (j > 0) issue_pv(2 * j - 2, v_prev);
-            if (t == 1 && j == 0 && no > 0) named_bar_sync(NB_START, 160);
             issue_s(sk, 2 * j);
             if (j > 0) {
               issue_pv(2 * j - 1, v_prev);
@@ -582,6 +588,9 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         if (!prefix && a.causal) lim = min(lim, sg.hidden + tok_in);
       }
       float m_used = -INFINITY, l = 0.f;
+      // The two softmax warpgroups take turns at their exponentials: side by side they would slow each other down
+      // into lockstep, and stores, waits and handoffs of both would leave the SM idle at the same time.
+      const int turns = 2 * min(sg.nj[0], sg.nj[1]);
       for (int c = 0; c < 2 * nt; ++c, ++cc) {
         const int sl = c & 1;
         const uint32_t s_c = s_addr + HN * sl;
@@ -599,17 +608,16 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < HN; ++e) x[e] = __uint_as_float(v[e]);
         }
-        const float* sc = scales + ((vi % C::NSLOT) >> 1) * 384 + HN * sl;
         if (INT8) {
+          const float* sc = scales + ((vi % C::NSLOT) >> 1) * 128 + HN * sl;
 #pragma unroll
           for (int e = 0; e < HN; e += 4) {
             const float4 k4 = *reinterpret_cast<const float4*>(sc + e);
-            const float4 v4 = *reinterpret_cast<const float4*>(sc + 128 + e);
-            f2unpack(f2fma(f2pack(x[e], x[e + 1]), f2pack(k4.x, k4.y), f2pack(v4.x, v4.y)), x[e], x[e + 1]);
-            f2unpack(f2fma(f2pack(x[e + 2], x[e + 3]), f2pack(k4.z, k4.w), f2pack(v4.z, v4.w)), x[e + 2], x[e + 3]);
+            f2unpack(f2mul(f2pack(x[e], x[e + 1]), f2pack(k4.x, k4.y)), x[e], x[e + 1]);
+            f2unpack(f2mul(f2pack(x[e + 2], x[e + 3]), f2pack(k4.z, k4.w)), x[e + 2], x[e + 3]);
           }
         }
-        const float cs = INT8 ? 1.0f : a.scale_log2;
+        const float cs = a.scale_log2;
         const int nv = max(0, min(lim - sg.key0 - c * HN, HN));
         if (!__all_sync(0xffffffffu, nv == HN)) {
 #pragma unroll
@@ -623,13 +631,14 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
             m_used = mt;
           }
         }
+        if (c < turns && (t == 1 || c > 0)) named_bar_sync(NB_TURN + t, 256);
         const float msub = (m_used == -INFINITY) ? 0.f : m_used - kPOffset;
         const uint64_t c2 = f2pack(cs, cs), nm2 = f2pack(-msub, -msub);
         uint32_t pk[HN / 2];
         uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int e = 0; e < HN; e += 2) {
-          const uint64_t y2 = INT8 ? f2add(f2pack(x[e], x[e + 1]), nm2) : f2fma(f2pack(x[e], x[e + 1]), c2, nm2);
+          const uint64_t y2 = f2fma(f2pack(x[e], x[e + 1]), c2, nm2);
           float p0, p1;
           if (((e >> 1) & 7) < kFmaPairs) {
             exp2_fma2(y2, p0, p1);
@@ -639,12 +648,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
             p0 = ex2_approx(y0);
             p1 = ex2_approx(y1);
           }
-          if (INT8) {
-            const float2 iv = *reinterpret_cast<const float2*>(sc + 256 + e);
-            acc2[(e >> 1) & 3] = f2fma(f2pack(p0, p1), f2pack(iv.x, iv.y), acc2[(e >> 1) & 3]);
-          } else {
-            acc2[(e >> 1) & 3] = f2add(acc2[(e >> 1) & 3], f2pack(p0, p1));
-          }
+          acc2[(e >> 1) & 3] = f2add(acc2[(e >> 1) & 3], f2pack(p0, p1));
           pk[e >> 1] = pack_half2(p0, p1);
         }
         {
@@ -653,6 +657,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           f2unpack(s2, s0, s1);
           l = l * alpha + (s0 + s1);
         }
+        if (c < turns && (t == 0 || c + 1 < turns)) named_bar_arrive(NB_TURN + 1 - t, 256);
         __syncwarp();
         tmem_st32p(s_c, pk);      // P(c) over the first 32 columns of its half
         // P.V(c - 1) must have completed before O is rescaled; phases up to
@@ -680,8 +685,8 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (t == 0 && c == 0 && sg.nj[1] > 0) named_bar_arrive(NB_START, 160);
-        named_bar_sync(NB_P + t, 160);
+        // not waiting: this half's next P follows an S that is issued behind this one's P.V
+        named_bar_arrive(NB_P + 2 * t + sl, 160);
       }
       n += sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
 
