@@ -57,8 +57,9 @@ struct CfgT {
   static constexpr int STAGES = NSLOT / 2;
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int OFF_SLOT = 2 * Q_BYTES;
-  static constexpr int OFF_SCALE = OFF_SLOT + NSLOT * SLOT;       // [STAGES][128] K scales
-  static constexpr int OFF_BAR = OFF_SCALE + STAGES * 128 * 4;
+  static constexpr int OFF_SCALE = OFF_SLOT + NSLOT * SLOT;      // [STAGES][128] K scales
+  static constexpr int OFF_STAGE = OFF_SCALE + STAGES * 128 * 4;  // 4 KB for each softmax warp: results on their way out
+  static constexpr int OFF_BAR = OFF_STAGE + 8 * 4096;
   static constexpr int SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t IDESC_S = idesc_f16(BM, 64, false);
   static constexpr uint32_t IDESC_PV = idesc_f16(BM, D, true);
@@ -698,10 +699,17 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         tc_fence_after();
         __syncwarp();
       }
-      const int64_t idx = sg.slot * total + static_cast<int64_t>(tok) * Hq + head;
-      if (row_ok && !direct) a.ml[idx] = make_float2(m_used, l);
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      const int64_t idx = static_cast<int64_t>(tok) * Hq + head;
+      if (row_ok && !direct) a.ml[sg.slot * total + idx] = make_float2(m_used, l);
+      const float inv = !direct ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
       if (nt > 0 || direct) {
+        // 32 columns of the warp's 32 rows at a time through shared memory, so that a store instruction writes
+        // four rows' whole 128-byte lines instead of 32 rows' halves of sectors
+        const uint32_t stage = sbase + C::OFF_STAGE + warp * 4096;
+        const int64_t mine = row_ok ? (direct ? tok * a.o_t + head * a.o_h : (sg.slot * total + idx) * D) : -1;
+        int64_t at[8];        // where rows lane / 8 + 4 i go
+#pragma unroll
+        for (int i = 0; i < 8; ++i) at[i] = __shfl_sync(0xffffffffu, mine, 4 * i + (lane >> 3));
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
@@ -712,23 +720,27 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
-          if (row_ok && direct) {
-            __half* dst = a.out + tok * a.o_t + head * a.o_h + q * 32;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t h[4];
+          for (int e = 0; e < 8; ++e)
+            sts128(stage + lane * 128 + ((e ^ (lane & 7)) << 4),
+                   make_uint4(__float_as_uint(__uint_as_float(o[4 * e]) * inv),
+                              __float_as_uint(__uint_as_float(o[4 * e + 1]) * inv),
+                              __float_as_uint(__uint_as_float(o[4 * e + 2]) * inv),
+                              __float_as_uint(__uint_as_float(o[4 * e + 3]) * inv)));
+          __syncwarp();
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                h[i] = pack_half2(__uint_as_float(o[e + 2 * i]) * inv, __uint_as_float(o[e + 2 * i + 1]) * inv);
-              *reinterpret_cast<uint4*>(dst + e) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-          } else if (row_ok) {
-            float* dst = a.o + idx * D + q * 32;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + (lane >> 3), e = lane & 7;
+            const uint4 v = lds128(stage + row * 128 + ((e ^ (row & 7)) << 4));
+            if (at[i] < 0) continue;
+            if (direct)
+              *reinterpret_cast<uint2*>(a.out + at[i] + q * 32 + e * 4) =
+                  make_uint2(pack_half2(__uint_as_float(v.x), __uint_as_float(v.y)),
+                             pack_half2(__uint_as_float(v.z), __uint_as_float(v.w)));
+            else
+              *reinterpret_cast<uint4*>(a.o + at[i] + q * 32 + e * 4) = v;
           }
-          __syncwarp();           // tensor-memory loads are the whole warp's
+          __syncwarp();           // tensor-memory loads and the stage are the whole warp's
         }
         tc_fence_before();      // these reads of O come before the next segment's first P.V
       }
