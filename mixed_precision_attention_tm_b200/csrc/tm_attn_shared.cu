@@ -23,10 +23,11 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t ba
   const int64_t own_units = ceil_div(max_kv_len, 128), pre_units = ceil_div(prefix_len, 128);
   p.own_rows = static_cast<int>(own_rows);
   p.pre_rows = static_cast<int>(pre_rows);
-  // split kernel: two waves of one CTA per SM, every CTA with about the same keys, at most 30 splits of each
+  // split kernel: pieces small enough for eight CTAs per SM, so that sequences of different lengths (known on the
+  // device alone) even out over the SMs; at most kMostSplits of each
   const int64_t split_units = (p.own_tile ? 0 : batch * own_rows * Hkv * own_units) +
                               (p.pre_tile ? 0 : pre_rows * Hkv * pre_units);
-  int64_t chunk = ceil_div(split_units, 2 * kSmsB200);
+  int64_t chunk = ceil_div(split_units, 8 * kSmsB200);
   if (chunk < 1) chunk = 1;
   if (p.pre_tile) {
     // equal pieces of the line of key tiles, one for each SM
@@ -65,8 +66,11 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t ba
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kStep = 32;     // keys of one warp step
+constexpr int kStep = 16;     // keys of one warp step: never more than one page
 constexpr int kStages = 3;
+// 2^kPOffset is the largest weight when the reference is the maximum; scores up
+// to 2^kLazy above it leave it alone: 2^15 at most, inside fp16.
+constexpr float kLazy = 15.0f - kPOffset;
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -92,7 +96,7 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return v;
 }
 
-// Bytes of one 32-key stage of K (V the same), and where the 16-byte piece c
+// Bytes of one 16-key stage of K (V the same), and where the 16-byte piece c
 // of key row `row` lies in it: permuted so that the reads below (ldmatrix of
 // eight rows; for INT8, 16-byte reads of two rows' quarters for K and of four
 // even or odd rows for V) meet no bank twice.
@@ -111,24 +115,28 @@ struct Stage {
 
 template <int D, bool INT8>
 constexpr int split_smem() {
-  return kWarps * kStages * (2 * Stage<D, INT8>::BYTES + (INT8 ? 2 * kStep * 4 : 0)) + kWarps * 16 * 8;
+  return kWarps * (kStages * (2 * Stage<D, INT8>::BYTES + (INT8 ? 3 * kStep * 4 : 0)) + 16 * 8);
 }
 
 // Attention of up to 16 packed rows over one range of keys.
 //
 // Decoding reads far more than it computes (a key's 2 d values serve g rows),
-// so this is built around the copies: each of the four warps owns every fourth
-// 32-key step and its own three-stage ring of cp.async copies, with no
-// barrier between warps until the join at the end.  At d = 128 in fp16 a stage
-// is 16 KB, so 128 KB per SM are in flight while a third of the ring is
-// computed on.  Rows of a step past the range's end are filled with zeros
-// and never read from memory.  The products run on mma.sync m16n8k16: 16 rows
+// so this is built around the copies: each warp owns every fourth 16-key step
+// and its own three-stage ring of cp.async copies, with no barrier between
+// warps until the join at the end.  A warp's step is a chain of dependent
+// instructions, so it takes several warps to keep up with the copies: at
+// d = 128 in fp16 two CTAs (eight warps, 192 KB of rings) fit an SM, else
+// more.  With two warps of 32-key steps per CTA the same batch (64 sequences of 64 to
+// 1024 tokens, 143 MB) took 43 us.  A step's keys lie in one page, so its copies need one
+// block-table entry.  Rows past the range's end are filled with zeros and
+// never read from memory.  The products run on mma.sync m16n8k16: 16 rows
 // hold a whole group of query heads, where a 128-row tensor-memory tile would
 // be nearly empty.
 //
 // INT8: K and V stay codes in shared memory and become fp16 in registers
-// (exactly); a key's K scale multiplies its scores and its V scale its P,
-// which costs two roundings fewer than scaling the codes.  The code layouts
+// (exactly).  With t_j = s_j ks_j + log2 vs_j the weights 2^(t_j - m) carry
+// the V scale, and the row sum takes 2^(t_j - m) / vs_j: no rounding is added
+// and the weights keep fp16's range whatever the scales are.  The code layouts
 // follow the fragments: the order of d within the QK^T sum is free, so a
 // lane's 16 consecutive codes serve four MMAs; the order of output columns is
 // free too, so a lane's n index stands for d / 8 consecutive dimensions.
@@ -244,8 +252,8 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
 
   uint8_t* ring = smem + warp * kStages * 2 * S::BYTES;
   const uint32_t ring_s = smem_u32(ring);
-  float* scales = reinterpret_cast<float*>(smem + kWarps * kStages * 2 * S::BYTES) + warp * kStages * 2 * kStep;
-  float2* ml_s = reinterpret_cast<float2*>(smem + kWarps * kStages * (2 * S::BYTES + (INT8 ? 2 * kStep * 4 : 0)));
+  float* scales = reinterpret_cast<float*>(smem + kWarps * kStages * 2 * S::BYTES) + warp * kStages * 3 * kStep;
+  float2* ml_s = reinterpret_cast<float2*>(smem + kWarps * kStages * (2 * S::BYTES + (INT8 ? 3 * kStep * 4 : 0)));
 
   const uint8_t* kbase = a.pool.k + kvh * a.pool.stride_h;
   const uint8_t* vbase = a.pool.v + kvh * a.pool.stride_h;
@@ -253,10 +261,10 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
   const int steps = first < k1 ? static_cast<int>((k1 - first + kWarps * kStep - 1) / (kWarps * kStep)) : 0;
   const int shift = a.pool.page_shift;
 
-  // page of this lane's key of step i, -1 where nothing is to be read
+  // page of step i, -1 where nothing is to be read
   auto page_at = [&](int i) -> int32_t {
-    const int64_t key = first + static_cast<int64_t>(i) * kWarps * kStep + lane;
-    if (i >= steps || key >= k1) return -1;
+    if (i >= steps) return -1;
+    const int64_t key = first + static_cast<int64_t>(i) * (kWarps * kStep);
     int32_t page;
     if (prefix) {
       page = __ldg(a.prefix_pages + (key >> shift));
@@ -264,36 +272,40 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
     } else {
       page = page_of(a.pt, b, key);
     }
-    if (page < 0) dev_error(err, TM_DEVERR_SEQLEN);
+    if (page < 0 && lane == 0) dev_error(err, TM_DEVERR_SEQLEN);
     return page;
   };
-  float pend_k = 0.f, pend_v = 0.f;
+  constexpr int RPI = 32 / S::PIECES;          // rows of one copy instruction
+  const int cp_c = lane % S::PIECES, cp_r = lane / S::PIECES;
+  const int64_t cp_off = cp_r * a.pool.stride_t + cp_c * 16;
+  float pend_k = 0.f, pend_v = 1.f;
   // copies of step i into its stage; the scales follow one call later
   auto issue = [&](int i, int32_t page) {
-    if (INT8 && i > 0) {
-      const int st = (i - 1) % kStages;
-      scales[st * 2 * kStep + lane] = pend_k;
-      scales[st * 2 * kStep + kStep + lane] = pend_v;
+    if (INT8 && i > 0 && lane < kStep) {
+      float* sc = scales + (i - 1) % kStages * 3 * kStep + lane;
+      const float f = pend_v == 0.f ? 5.9604645e-8f : pend_v;   // a zero scale (codes all 0) counts in the row sum alone
+      sc[0] = pend_k * a.scale_log2;
+      sc[kStep] = log2f(f);
+      sc[2 * kStep] = 1.0f / f;
     }
     if (i < steps) {
-      const int64_t key = first + static_cast<int64_t>(i) * kWarps * kStep + lane;
+      const int64_t key = first + static_cast<int64_t>(i) * (kWarps * kStep);
       const int64_t s = key & ((1 << shift) - 1);
-      const int64_t off = page >= 0 ? page * a.pool.stride_page + s * a.pool.stride_t : -1;
+      const int valid = page >= 0 ? static_cast<int>(k1 - key < kStep ? k1 - key : kStep) : 0;
+      const int64_t off = valid > 0 ? page * a.pool.stride_page + s * a.pool.stride_t : 0;
       if (INT8) {
-        const int64_t so = page * a.pool.sstride_page + s * a.pool.sstride_t + kvh * a.pool.sstride_h;
-        pend_k = page >= 0 ? __half2float(a.pool.ks[so]) : 0.f;
-        pend_v = page >= 0 ? __half2float(a.pool.vs[so]) : 0.f;
+        const int64_t so = page * a.pool.sstride_page + (s + lane) * a.pool.sstride_t + kvh * a.pool.sstride_h;
+        pend_k = lane < valid ? __half2float(a.pool.ks[so]) : 0.f;
+        pend_v = lane < valid ? __half2float(a.pool.vs[so]) : 0.f;
       }
       const uint32_t dst = ring_s + (i % kStages) * 2 * S::BYTES;
-      constexpr int RPI = 32 / S::PIECES;
-      const int c = lane % S::PIECES;
 #pragma unroll
       for (int n = 0; n < kStep / RPI; ++n) {
-        const int row = n * RPI + lane / S::PIECES;
-        const int64_t o = __shfl_sync(0xffffffffu, off, row);
-        const bool real = o >= 0;
-        cp16(dst + S::at(row, c, false), kbase + (real ? o + c * 16 : 0), real);
-        cp16(dst + S::BYTES + S::at(row, c, true), vbase + (real ? o + c * 16 : 0), real);
+        const int row = n * RPI + cp_r;
+        const bool real = row < valid;
+        const int64_t at = real ? off + cp_off + n * RPI * a.pool.stride_t : 0;
+        cp16(dst + S::at(row, cp_c, false), kbase + at, real);
+        cp16(dst + S::BYTES + S::at(row, cp_c, true), vbase + at, real);
       }
     }
     cp_commit();
@@ -316,55 +328,65 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
     page = page_at(i + 3);
     const uint32_t ks_s = ring_s + (i % kStages) * 2 * S::BYTES;
     const uint32_t vs_s = ks_s + S::BYTES;
-    const float* sc = scales + (i % kStages) * 2 * kStep;
-    const int64_t key0 = first + static_cast<int64_t>(i) * kWarps * kStep;
+    const float* sc = scales + (i % kStages) * 3 * kStep + 2 * quad;
+    const int64_t key0 = first + static_cast<int64_t>(i) * (kWarps * kStep);
 
-    float s[4][4];
+    // even and odd halves of d in sums of their own: half the chain of dependent MMAs
+    float s[2][4], s2[2][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[j][e] = s2[j][e] = 0.f;
+    }
     if (!INT8) {
 #pragma unroll
       for (int ks = 0; ks < KS; ks += 2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
           uint32_t bfr[4];
           ldsm4(ks_s + S::at(8 * j + (lane & 7), 2 * ks + (lane >> 3), false), bfr);
           mma16816(s[j], qf[ks], bfr[0], bfr[1]);
-          mma16816(s[j], qf[ks + 1], bfr[2], bfr[3]);
+          mma16816(s2[j], qf[ks + 1], bfr[2], bfr[3]);
         }
       }
     } else {
 #pragma unroll
       for (int c = 0; c < KS / 4; ++c) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
           const uint4 v = lds128(ks_s + S::at(8 * j + r8, 4 * c + quad, false));
           const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            mma16816(s[j], qf[4 * c + e], codes2(w[e], 0x4140u), codes2(w[e], 0x4342u));
+            mma16816(e & 1 ? s2[j] : s[j], qf[4 * c + e], codes2(w[e], 0x4140u), codes2(w[e], 0x4342u));
         }
       }
     }
 
     // scores in powers of two; hidden keys to -inf by selection, whatever they hold
-    float x[4][4];
+    float x[2][4], iv[2][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float k0s = a.scale_log2, k1s = a.scale_log2;
+    for (int j = 0; j < 2; ++j) {
+      float k0s = a.scale_log2, k1s = a.scale_log2, v0 = 0.f, v1 = 0.f;
       if (INT8) {
-        const float2 f = *reinterpret_cast<const float2*>(sc + 8 * j + 2 * quad);
-        k0s *= f.x;
-        k1s *= f.y;
+        const float2 fk = *reinterpret_cast<const float2*>(sc + 8 * j);
+        const float2 fv = *reinterpret_cast<const float2*>(sc + kStep + 8 * j);
+        const float2 fi = *reinterpret_cast<const float2*>(sc + 2 * kStep + 8 * j);
+        k0s = fk.x;
+        k1s = fk.y;
+        v0 = fv.x;
+        v1 = fv.y;
+        iv[j][0] = fi.x;
+        iv[j][1] = fi.y;
       }
-      x[j][0] = s[j][0] * k0s;
-      x[j][1] = s[j][1] * k1s;
-      x[j][2] = s[j][2] * k0s;
-      x[j][3] = s[j][3] * k1s;
+      x[j][0] = (s[j][0] + s2[j][0]) * k0s + v0;
+      x[j][1] = (s[j][1] + s2[j][1]) * k1s + v1;
+      x[j][2] = (s[j][2] + s2[j][2]) * k0s + v0;
+      x[j][3] = (s[j][3] + s2[j][3]) * k1s + v1;
     }
     if (key0 + kStep > open) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 2; ++j) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int64_t key = key0 + 8 * j + 2 * quad + (e & 1);
@@ -372,31 +394,21 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
         }
       }
     }
-    float scale[2];
+    // the references are raised (and O and l rescaled) only when a score exceeds one by 2^kLazy
+    float mx[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float mx = -INFINITY;
+    for (int h = 0; h < 2; ++h) mx[h] = fmaxf(fmaxf(x[0][2 * h], x[0][2 * h + 1]), fmaxf(x[1][2 * h], x[1][2 * h + 1]));
+    if (__any_sync(0xffffffffu, mx[0] > m[0] + kLazy || mx[1] > m[1] + kLazy)) {
+      float scale[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(x[j][2 * h], x[j][2 * h + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[h], mx);
-      const float use = mn == -INFINITY ? 0.f : mn;
-      scale[h] = ex2_approx(m[h] - use);
-      m[h] = mn;
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float pr = ex2_approx(x[j][2 * h + e] - use + kPOffset);
-          x[j][2 * h + e] = pr;
-          sum += pr;
-        }
+      for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        const float mn = fmaxf(m[h], mx[h]);
+        scale[h] = ex2_approx(m[h] - (mn == -INFINITY ? 0.f : mn));
+        m[h] = mn;
+        l[h] *= scale[h];
       }
-      l[h] = l[h] * scale[h] + sum;
-    }
-    if (__any_sync(0xffffffffu, scale[0] != 1.f || scale[1] != 1.f)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         o[n][0] *= scale[0];
@@ -406,56 +418,57 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
       }
     }
 #pragma unroll
-    for (int k2 = 0; k2 < 2; ++k2) {
-      if (INT8) {
+    for (int h = 0; h < 2; ++h) {
+      const float use = (m[h] == -INFINITY ? 0.f : m[h]) - kPOffset;
+      float sum = 0.f;
 #pragma unroll
-        for (int j = 2 * k2; j < 2 * k2 + 2; ++j) {
-          const float2 f = *reinterpret_cast<const float2*>(sc + kStep + 8 * j + 2 * quad);
-          x[j][0] *= f.x;
-          x[j][1] *= f.y;
-          x[j][2] *= f.x;
-          x[j][3] *= f.y;
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float pr = ex2_approx(x[j][2 * h + e] - use);
+          x[j][2 * h + e] = pr;
+          sum += INT8 ? pr * iv[j][e] : pr;
         }
       }
-      const uint32_t pf[4] = {pack_half2(x[2 * k2][0], x[2 * k2][1]), pack_half2(x[2 * k2][2], x[2 * k2][3]),
-                              pack_half2(x[2 * k2 + 1][0], x[2 * k2 + 1][1]),
-                              pack_half2(x[2 * k2 + 1][2], x[2 * k2 + 1][3])};
-      if (!INT8) {
+      l[h] += sum;
+    }
+    const uint32_t pf[4] = {pack_half2(x[0][0], x[0][1]), pack_half2(x[0][2], x[0][3]), pack_half2(x[1][0], x[1][1]),
+                            pack_half2(x[1][2], x[1][3])};
+    if (!INT8) {
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-          uint32_t bfr[4];
-          ldsm4t(vs_s + S::at(16 * k2 + ((lane >> 3) & 1) * 8 + (lane & 7), n + (lane >> 4), true), bfr);
-          mma16816(o[n], pf, bfr[0], bfr[1]);
-          mma16816(o[n + 1], pf, bfr[2], bfr[3]);
+      for (int n = 0; n < NT; n += 2) {
+        uint32_t bfr[4];
+        ldsm4t(vs_s + S::at(((lane >> 3) & 1) * 8 + (lane & 7), n + (lane >> 4), true), bfr);
+        mma16816(o[n], pf, bfr[0], bfr[1]);
+        mma16816(o[n + 1], pf, bfr[2], bfr[3]);
+      }
+    } else {
+      // keys 2 quad, 2 quad + 1, 2 quad + 8, 2 quad + 9 of the 16; this lane's n index r8 stands for
+      // dimensions r8 * (D / 8) + n of n-tile n
+      uint32_t w[4][D / 32];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = 2 * quad + (e & 1) + 8 * (e >> 1);
+        if (D == 128) {
+          const uint4 v = lds128(vs_s + S::at(row, r8, true));
+          w[e][0] = v.x ^ 0x80808080u;
+          w[e][1] = v.y ^ 0x80808080u;
+          w[e][D / 32 - 2] = v.z ^ 0x80808080u;
+          w[e][D / 32 - 1] = v.w ^ 0x80808080u;
+        } else {
+          const uint2 v = lds64(vs_s + S::at(row, r8 >> 1, true) + (r8 & 1) * 8);
+          w[e][0] = v.x ^ 0x80808080u;
+          w[e][1] = v.y ^ 0x80808080u;
         }
-      } else {
-        // keys 2 quad, 2 quad + 1, 2 quad + 8, 2 quad + 9 of the 16; this lane's n index r8 stands for
-        // dimensions r8 * (D / 8) + n of n-tile n
-        uint32_t w[4][D / 32];
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = 16 * k2 + 2 * quad + (e & 1) + 8 * (e >> 1);
-          if (D == 128) {
-            const uint4 v = lds128(vs_s + S::at(row, r8, true));
-            w[e][0] = v.x ^ 0x80808080u;
-            w[e][1] = v.y ^ 0x80808080u;
-            w[e][D / 32 - 2] = v.z ^ 0x80808080u;
-            w[e][D / 32 - 1] = v.w ^ 0x80808080u;
-          } else {
-            const uint2 v = lds64(vs_s + S::at(row, r8 >> 1, true) + (r8 & 1) * 8);
-            w[e][0] = v.x ^ 0x80808080u;
-            w[e][1] = v.y ^ 0x80808080u;
-          }
-        }
+      for (int q = 0; q < D / 32; ++q) {
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-#pragma unroll
-          for (int hlf = 0; hlf < 2; ++hlf) {
-            const uint32_t lo = __byte_perm(w[0][q], w[1][q], hlf ? 0x7362u : 0x5140u);
-            const uint32_t hi = __byte_perm(w[2][q], w[3][q], hlf ? 0x7362u : 0x5140u);
-            mma16816(o[4 * q + 2 * hlf], pf, codes2(lo, 0x4140u), codes2(hi, 0x4140u));
-            mma16816(o[4 * q + 2 * hlf + 1], pf, codes2(lo, 0x4342u), codes2(hi, 0x4342u));
-          }
+        for (int hlf = 0; hlf < 2; ++hlf) {
+          const uint32_t lo = __byte_perm(w[0][q], w[1][q], hlf ? 0x7362u : 0x5140u);
+          const uint32_t hi = __byte_perm(w[2][q], w[3][q], hlf ? 0x7362u : 0x5140u);
+          mma16816(o[4 * q + 2 * hlf], pf, codes2(lo, 0x4140u), codes2(hi, 0x4140u));
+          mma16816(o[4 * q + 2 * hlf + 1], pf, codes2(lo, 0x4342u), codes2(hi, 0x4342u));
         }
       }
     }
@@ -473,6 +486,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
     ml_s[warp * 16 + r8 + 8] = make_float2(m[1], l[1]);
   }
   __syncwarp();
+  static_assert(NT * 32 * 16 <= kStages * 2 * S::BYTES, "a warp's O fits its ring");
   float* os = reinterpret_cast<float*>(ring);    // this warp's ring, no longer read
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -557,71 +571,100 @@ __global__ void __launch_bounds__(kWarps * 32) split_kernel(const __grid_constan
   pdl_wait();      // whoever waits for this kernel has waited for the one before it
 }
 
-// Joins a row's splits: one warp per (token, query head), the slots' (m, l)
-// across the lanes, then the O rows that carry weight.
-template <int D>
+// Joins a row's results: W warps per (token, query head).  Every warp weighs
+// all slots (one or two per lane); warp w adds the O rows of slots w, w + W, ..,
+// four loads in flight, and the warps' sums meet in shared memory.  Moves
+// count * d * 4 bytes a row, mostly out of L2; with few rows it is bound by
+// latency, which is what W is for.
+template <int D, int W>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ SharedArgs a) {
+  constexpr int V = D / 32;
+  __shared__ float sums[W > 1 ? 8 : 1][D];
   const int Hq = a.pool.H * a.plan.group;
   const int64_t total = a.T * Hq;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= total) return;
-  const int64_t t = row / Hq;
-  if (t >= rows_in_use(a) || (a.cu != nullptr && t < __ldg(a.cu))) return;
-  constexpr int V = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (8 / W) + warp / W;
+  const int part = warp % W;
+  const int t = static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(Hq));     // rows stay below 2^30
+  const bool live_row = row < total && t < rows_in_use(a) && (a.cu == nullptr || t >= __ldg(a.cu));
   const SharedPlan& p = a.plan;
   // prefix results of this row: the pieces of the line that its row block's key tiles lie in
   int pre = p.pre_splits;
   if (p.pre_tile) {
-    const int h = static_cast<int>(row - t * Hq);
-    const int64_t packed = t * p.group + h % p.group;
-    const int64_t first = (static_cast<int64_t>(h / p.group) * p.pre_rows + packed / 256) * p.pre_tiles;
-    pre = static_cast<int>((first + p.pre_tiles - 1) / p.pre_chunk - first / p.pre_chunk) + 1;
+    const int h = static_cast<int>(row) - t * Hq, kvh = h / p.group;
+    const int packed = t * p.group + h - kvh * p.group;
+    const int first = (kvh * p.pre_rows + packed / 256) * p.pre_tiles;
+    pre = (first + p.pre_tiles - 1) / p.pre_chunk - first / p.pre_chunk + 1;
   }
-  const int count = pre + p.own_splits;
+  const int count = live_row ? pre + p.own_splits : 0;
+  const int own_at = p.pre_splits - pre;      // result i lies in slot i, or i + own_at from `pre` on
   pdl_wait();
-  float acc[V] = {}, M = -INFINITY, L = 0.f;
-  for (int s0 = 0; s0 < count; s0 += 32) {
-    const int n = count - s0 < 32 ? count - s0 : 32;
-    const int own_at = p.pre_splits - pre;      // result i lies in slot i, or i + own_at from `pre` on
+  float m[2], wgt[2], M = -INFINITY, L = 0.f;
+  static_assert(2 * (kMostSplits + 2) <= 64, "two slots per lane");
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = lane + 32 * k;
     float2 ml = make_float2(-INFINITY, 0.f);
-    if (lane < n) ml = a.ml[(s0 + lane + (s0 + lane < pre ? 0 : own_at)) * total + row];
-    float mx = ml.x;
+    if (i < count) ml = a.ml[(i + (i < pre ? 0 : own_at)) * total + row];
+    m[k] = ml.x;
+    wgt[k] = ml.y;
+    M = fmaxf(M, ml.x);
+  }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float mn = fmaxf(M, mx);
-    const float use = mn == -INFINITY ? 0.f : mn;
-    const float keep = ex2_approx(M - use);
-    const float w = ml.y == 0.f ? 0.f : ex2_approx(ml.x - use);
-    float sum = w * ml.y;
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    L = L * keep + sum;
-    M = mn;
+  for (int k = 0; k < 2; ++k) {
+    const float l = wgt[k];
+    wgt[k] = l == 0.f ? 0.f : ex2_approx(m[k] - (M == -INFINITY ? 0.f : M));
+    L += wgt[k] * l;
+  }
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] *= keep;
-    unsigned live = __ballot_sync(0xffffffffu, w != 0.f);   // NaN counts as live
-    while (live) {
-      const int s = __ffs(live) - 1;
-      live &= live - 1;
-      const float ws = __shfl_sync(0xffffffffu, w, s);
-      const int slot = s0 + s + (s0 + s < pre ? 0 : own_at);
-      const float* src = a.o + (slot * total + row) * D + lane * V;
-      if (V == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(src);
-        acc[0] += ws * f.x;
-        acc[1] += ws * f.y;
-        acc[V - 2] += ws * f.z;
-        acc[V - 1] += ws * f.w;
-      } else {
-        const float2 f = *reinterpret_cast<const float2*>(src);
-        acc[0] += ws * f.x;
-        acc[1] += ws * f.y;
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  float acc[V] = {};
+  for (int i0 = part; i0 < count; i0 += 4 * W) {
+    float w[4], f[4][V];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * W;
+      w[k] = __shfl_sync(0xffffffffu, i < 32 ? wgt[0] : wgt[1], i & 31);
+      if (i >= count) w[k] = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[k][v] = 0.f;
+      if (w[k] != 0.f) {      // NaN counts
+        const float* src = a.o + ((i + (i < pre ? 0 : own_at)) * total + row) * D + lane * V;
+        if (V == 4) {
+          const float4 q = __ldcs(reinterpret_cast<const float4*>(src));
+          f[k][0] = q.x;
+          f[k][1] = q.y;
+          f[k][V - 2] = q.z;
+          f[k][V - 1] = q.w;
+        } else {
+          const float2 q = __ldcs(reinterpret_cast<const float2*>(src));
+          f[k][0] = q.x;
+          f[k][1] = q.y;
+        }
       }
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += w[k] * f[k][v];
+    }
   }
+  if (W > 1) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) sums[warp][lane * V + v] = acc[v];
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += sums[W > 1 ? warp + w : 0][lane * V + v];
+    }
+  }
+  if (!live_row) return;
   const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-  __half* dst = a.out + t * a.o_t + (row - t * Hq) * a.o_h + lane * V;
+  __half* dst = a.out + t * a.o_t + (static_cast<int>(row) - t * Hq) * a.o_h + lane * V;
   if (V == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_half2(acc[0] * inv, acc[1] * inv),
                                                 pack_half2(acc[V - 2] * inv, acc[V - 1] * inv));
@@ -661,8 +704,11 @@ tm_status launch(const SharedArgs& a, int d, bool int8, DevErr err, cudaStream_t
     after = true;
   }
   if (st != TM_OK || p.slots == 1) return st;
-  const int64_t blocks = (a.T * a.pool.H * p.group + 7) / 8;
-  return launch_kernel(d == 128 ? join_kernel<128> : join_kernel<64>, blocks, 256, 0, after, stream, a);
+  const int64_t rows = a.T * a.pool.H * p.group;
+  const int W = p.slots <= 2 || rows >= 8192 ? 1 : (rows >= 1024 ? 4 : 8);
+  auto join = d == 128 ? (W == 1 ? join_kernel<128, 1> : W == 4 ? join_kernel<128, 4> : join_kernel<128, 8>)
+                       : (W == 1 ? join_kernel<64, 1> : W == 4 ? join_kernel<64, 4> : join_kernel<64, 8>);
+  return launch_kernel(join, ceil_div(rows, 8 / W), 256, 0, after, stream, a);
 }
 
 bool plan_args_ok(int64_t T, int32_t Hq, int32_t Hkv, int32_t batch, int64_t max_seqlen, int64_t prefix_len,
