@@ -571,6 +571,92 @@ __global__ void __launch_bounds__(kWarps * 32) split_kernel(const __grid_constan
   pdl_wait();      // whoever waits for this kernel has waited for the one before it
 }
 
+// Results of one row (token t, query head h): prefix results lie in slots 0 ..
+// pre - 1, the pieces of the line that the row block's key tiles lie in.
+__device__ __forceinline__ int prefix_results(const SharedPlan& p, int t, int h) {
+  if (!p.pre_tile) return p.pre_splits;
+  const int kvh = h / p.group;
+  const int packed = t * p.group + h - kvh * p.group;
+  const int first = (kvh * p.pre_rows + packed / 256) * p.pre_tiles;
+  return (first + p.pre_tiles - 1) / p.pre_chunk - first / p.pre_chunk + 1;
+}
+
+// Joins the results of many rows: eight lanes per row, four results at a time
+// (their weights first, then the O rows that carry one).  Bound by the O rows,
+// 512 bytes of each result at d = 128.
+template <int D>
+__global__ void __launch_bounds__(256) join_rows_kernel(const __grid_constant__ SharedArgs a) {
+  constexpr int V = D / 32;      // 16-byte pieces of a lane
+  const SharedPlan& p = a.plan;
+  const int Hq = a.pool.H * p.group;
+  const int64_t total = a.T * Hq;
+  const int row = static_cast<int>(blockIdx.x) * 32 + (threadIdx.x >> 3);
+  const int lane = threadIdx.x & 7;
+  const int t = row / Hq, h = row - t * Hq;
+  const bool live_row = row < total && t < rows_in_use(a) && (a.cu == nullptr || t >= __ldg(a.cu));
+  const int pre = prefix_results(p, t, h);
+  const int count = live_row ? pre + p.own_splits : 0;
+  const int own_at = p.pre_splits - pre;      // result i lies in slot i, or i + own_at from `pre` on
+  pdl_wait();
+  float M = -INFINITY, L = 0.f;
+  float4 acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < count; i0 += 4) {
+    float2 ml[4];
+    float4 f[4][V];
+    float mx = M;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (i < count) ml[k] = a.ml[(i + (i < pre ? 0 : own_at)) * total + row];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k;
+      mx = fmaxf(mx, ml[k].x);
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[k][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (ml[k].y != 0.f) {      // NaN counts
+        const float4* src = reinterpret_cast<const float4*>(a.o + ((i + (i < pre ? 0 : own_at)) * total + row) * D) + lane;
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[k][v] = __ldcs(src + 8 * v);
+      }
+    }
+    const float use = mx == -INFINITY ? 0.f : mx;
+    const float keep = ex2_approx(M - use);
+    M = mx;
+    L *= keep;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      acc[v].x *= keep;
+      acc[v].y *= keep;
+      acc[v].z *= keep;
+      acc[v].w *= keep;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float w = ml[k].y == 0.f ? 0.f : ex2_approx(ml[k].x - use);
+      L += w * ml[k].y;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        acc[v].x += w * f[k][v].x;
+        acc[v].y += w * f[k][v].y;
+        acc[v].z += w * f[k][v].z;
+        acc[v].w += w * f[k][v].w;
+      }
+    }
+  }
+  if (!live_row) return;
+  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+  __half* dst = a.out + t * a.o_t + h * a.o_h + lane * 4;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    *reinterpret_cast<uint2*>(dst + 32 * v) = make_uint2(pack_half2(acc[v].x * inv, acc[v].y * inv),
+                                                         pack_half2(acc[v].z * inv, acc[v].w * inv));
+}
+
 // Joins a row's results: W warps per (token, query head).  Every warp weighs
 // all slots (one or two per lane); warp w adds the O rows of slots w, w + W, ..,
 // four loads in flight, and the warps' sums meet in shared memory.  Moves
@@ -579,7 +665,7 @@ __global__ void __launch_bounds__(kWarps * 32) split_kernel(const __grid_constan
 template <int D, int W>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ SharedArgs a) {
   constexpr int V = D / 32;
-  __shared__ float sums[W > 1 ? 8 : 1][D];
+  __shared__ float sums[8][D];
   const int Hq = a.pool.H * a.plan.group;
   const int64_t total = a.T * Hq;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -588,14 +674,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Share
   const int t = static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(Hq));     // rows stay below 2^30
   const bool live_row = row < total && t < rows_in_use(a) && (a.cu == nullptr || t >= __ldg(a.cu));
   const SharedPlan& p = a.plan;
-  // prefix results of this row: the pieces of the line that its row block's key tiles lie in
-  int pre = p.pre_splits;
-  if (p.pre_tile) {
-    const int h = static_cast<int>(row) - t * Hq, kvh = h / p.group;
-    const int packed = t * p.group + h - kvh * p.group;
-    const int first = (kvh * p.pre_rows + packed / 256) * p.pre_tiles;
-    pre = (first + p.pre_tiles - 1) / p.pre_chunk - first / p.pre_chunk + 1;
-  }
+  const int pre = prefix_results(p, t, static_cast<int>(row) - t * Hq);
   const int count = live_row ? pre + p.own_splits : 0;
   const int own_at = p.pre_splits - pre;      // result i lies in slot i, or i + own_at from `pre` on
   pdl_wait();
@@ -651,16 +730,14 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Share
       for (int v = 0; v < V; ++v) acc[v] += w[k] * f[k][v];
     }
   }
-  if (W > 1) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) sums[warp][lane * V + v] = acc[v];
-    __syncthreads();
-    if (part != 0) return;
+  for (int v = 0; v < V; ++v) sums[warp][lane * V + v] = acc[v];
+  __syncthreads();
+  if (part != 0) return;
 #pragma unroll
-    for (int w = 1; w < W; ++w) {
+  for (int w = 1; w < W; ++w) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += sums[W > 1 ? warp + w : 0][lane * V + v];
-    }
+    for (int v = 0; v < V; ++v) acc[v] += sums[warp + w][lane * V + v];
   }
   if (!live_row) return;
   const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
@@ -705,9 +782,10 @@ tm_status launch(const SharedArgs& a, int d, bool int8, DevErr err, cudaStream_t
   }
   if (st != TM_OK || p.slots == 1) return st;
   const int64_t rows = a.T * a.pool.H * p.group;
-  const int W = p.slots <= 2 || rows >= 8192 ? 1 : (rows >= 1024 ? 4 : 8);
-  auto join = d == 128 ? (W == 1 ? join_kernel<128, 1> : W == 4 ? join_kernel<128, 4> : join_kernel<128, 8>)
-                       : (W == 1 ? join_kernel<64, 1> : W == 4 ? join_kernel<64, 4> : join_kernel<64, 8>);
+  if (rows >= 8192 || p.slots <= 2)
+    return launch_kernel(d == 128 ? join_rows_kernel<128> : join_rows_kernel<64>, ceil_div(rows, 32), 256, 0, after, stream, a);
+  const int W = rows >= 1024 ? 4 : 8;
+  auto join = d == 128 ? (W == 4 ? join_kernel<128, 4> : join_kernel<128, 8>) : (W == 4 ? join_kernel<64, 4> : join_kernel<64, 8>);
   return launch_kernel(join, ceil_div(rows, 8 / W), 256, 0, after, stream, a);
 }
 

@@ -15,8 +15,8 @@
 // is copied row by row (cp.async) instead, the rows past the end as zeros, so
 // that nothing behind a sequence's end is ever used.
 //
-// INT8 pages: the copies bring the codes, which four more warps turn into fp16
-// in place.  K stays codes (exactly) and a key's scale multiplies its scores in
+// INT8 pages: the copies bring the codes, which two more warpgroups (one
+// for K, one for V) turn into fp16 in place.  K stays codes (exactly) and a key's scale multiplies its scores in
 // fp32; V becomes fp16(code * scale), the value that tm_kv_gather gives: its one
 // rounding is of the size of P's, and carrying V's scale in P instead would take
 // a second pass of 128-byte shared-memory reads through the softmax and fp16's
@@ -54,7 +54,7 @@ struct CfgT {
   static constexpr int HALF = 128 * 128;               // one 64-column slab of a tile
   static constexpr int SLOT = BN * D * 2;              // an fp16 K or V tile
   static constexpr int NSLOT = 131072 / SLOT;          // 4 (d = 128) or 8 (d = 64)
-  static constexpr int STAGES = NSLOT / 2;
+  static constexpr int STAGES = NSLOT / 2 + 1;         // of K scales
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int OFF_SLOT = 2 * Q_BYTES;
   static constexpr int OFF_SCALE = OFF_SLOT + NSLOT * SLOT;      // [STAGES][128] K scales
@@ -65,10 +65,10 @@ struct CfgT {
   static constexpr uint32_t IDESC_PV = idesc_f16(BM, D, true);
   static constexpr int CODES = BN * D;                 // INT8: a K or V tile's codes, in the slot's upper half
   static constexpr int LOADED = INT8 ? CODES : SLOT;   // bytes that a tile's copies bring
-  // Registers at launch, and after the split over softmax, control and (INT8) conversion warpgroups.
-  static constexpr int THREADS = INT8 ? 512 : 384, LAUNCH_REGS = INT8 ? 128 : 168;
-  static constexpr int SOFTMAX_REGS = INT8 ? 200 : 216, CONTROL_REGS = INT8 ? 56 : 72, CONVERT_REGS = INT8 ? 56 : 0;
-  static_assert(2 * 128 * SOFTMAX_REGS + 128 * CONTROL_REGS + 128 * CONVERT_REGS == THREADS * LAUNCH_REGS,
+  // Registers at launch, and after the split over softmax, control and (INT8) two conversion warpgroups.
+  static constexpr int THREADS = INT8 ? 640 : 384, LAUNCH_REGS = INT8 ? 96 : 168;
+  static constexpr int SOFTMAX_REGS = INT8 ? 168 : 216, CONTROL_REGS = INT8 ? 64 : 72, CONVERT_REGS = INT8 ? 40 : 0;
+  static_assert(2 * 128 * SOFTMAX_REGS + 128 * CONTROL_REGS + 256 * CONVERT_REGS == THREADS * LAUNCH_REGS,
                 "register split");
   static_assert(SMEM <= 232448, "shared memory per CTA");
   __host__ __device__ static constexpr uint32_t s_col(int t) { return 128u * t; }
@@ -252,68 +252,78 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
   // Page of key `key` of a segment: -1 behind its end, -2 where it cannot be used
   const int shift = a.pool.page_shift;
   const int page_mask = (1 << shift) - 1;
+  auto entry_at = [&](const Segment& s, int key) -> int32_t {     // as the table has it
+    const int col = key >> shift;
+    if (key >= s.lk || (!prefix && col >= a.pt.cols)) return -1;
+    return __ldg(prefix ? a.prefix_pages + col : a.pt.table + s.b * a.pt.stride + col);
+  };
   auto page_at = [&](const Segment& s, int key) -> int32_t {
     if (key >= s.lk) return -1;
-    const int col = key >> shift;
-    int32_t page;
-    if (prefix) page = __ldg(a.prefix_pages + col);
-    else page = col < a.pt.cols ? __ldg(a.pt.table + s.b * a.pt.stride + col) : -1;
+    const int32_t page = entry_at(s, key);
     return page_ok(page, a.pool.num_pages) ? page : -2;
   };
 
   if (INT8 && warp >= 12) {
-    // ======================= conversion of codes (thread r: key row r of each tile) ====
+    // ======================= conversion of codes (warpgroup v: K or V; thread r: key row r of each tile) ====
     regs_dec<C::CONVERT_REGS>();
-    const int r = threadIdx.x - 384;
-    uint32_t n = 0;
+    const int v = (warp - 12) >> 2;
+    const int r = threadIdx.x & 127;
+    const __half* const scale_of = (v ? a.pool.vs : a.pool.ks);
+    uint32_t i = v;
     while (next_segment(u, sg)) {
       const int nj = sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
-      auto scales_of = [&](int j, float& ks, __half& vs) {
-        const int key = sg.key0 + j * 128 + r;
-        const int32_t page = j < nj ? page_at(sg, key) : -1;
-        ks = 0.f;
-        vs = __float2half(0.f);
-        if (page < 0) return;
-        const int64_t so = page * a.pool.sstride_page + (key & page_mask) * a.pool.sstride_t + sg.kvh * a.pool.sstride_h;
-        ks = __half2float(a.pool.ks[so]);
-        vs = a.pool.vs[so];
+      // this row's page and scale, loaded two and one key tiles ahead
+      auto entry_of = [&](int j) { return j < nj ? entry_at(sg, sg.key0 + j * 128 + r) : -1; };
+      auto scale_at = [&](int j, int32_t page) -> __half {
+        if (!page_ok(page, a.pool.num_pages)) return __float2half(0.f);
+        return scale_of[page * a.pool.sstride_page + ((sg.key0 + j * 128 + r) & page_mask) * a.pool.sstride_t +
+                        sg.kvh * a.pool.sstride_h];
       };
-      float ks, ks_next;
-      __half vs, vs_next;
-      scales_of(0, ks_next, vs_next);
-      for (int j = 0; j < nj; ++j, ++n) {
-        ks = ks_next;
-        vs = vs_next;
-        scales_of(j + 1, ks_next, vs_next);
-#pragma unroll 1
-        for (int v = 0; v < 2; ++v) {
-          const uint32_t i = 2 * n + v, slot = i % C::NSLOT;
+      int32_t entry = entry_of(0);
+      __half next = scale_at(0, entry);
+      entry = entry_of(1);
+      for (int j = 0; j < nj; ++j, i += 2) {
+        const __half scale = next;
+        next = scale_at(j + 1, entry);
+        entry = entry_of(j + 2);
+        {
+          const uint32_t slot = i % C::NSLOT;
           mbar_wait_warp(bar(T_CODES + slot), (i / C::NSLOT) & 1, err, abort_flag);
           const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT;
-          if (v) scales[(slot >> 1) * 128 + r] = ks;     // the V tile's release frees its stage of scales
-          const __half2 by = __half2half2(v ? vs : __float2half(1.f));
-          // d = 128: the codes lie where the upper 64 columns go, row r's in row r's place, and are read before
-          // that is written.  d = 64: 64-byte rows over other rows' places, so all are read first.
-#pragma unroll
-          for (int half = 0; half < D / 64; ++half) {
-            const uint32_t src = D == 128 ? tile + C::HALF + r * 128 : tile + C::CODES + r * 64;
-            const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
+          // K's scales outlive its slot: the softmax reads those of key tile j until P(2 j + 1).  With one stage more
+          // than the ring has key tiles, the next tile in this stage lands behind a release of key tile j + 1, whose
+          // last S is issued behind P.V(2 j + 1).
+          if (v == 0) scales[((i / 2) % C::STAGES) * 128 + r] = __half2float(scale);
+          const __half2 by = __half2half2(v ? scale : __float2half(1.f));
+          auto widen = [&](uint4 c, uint32_t at, int q) {      // 16 codes to pieces 2 q and 2 q + 1 of a row
+            const uint32_t x[4] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u};
+            sts128(at + (((2 * q) ^ (r & 7)) << 4),
+                   make_uint4(scaled2(x[0], 0x4140u, by), scaled2(x[0], 0x4342u, by), scaled2(x[1], 0x4140u, by),
+                              scaled2(x[1], 0x4342u, by)));
+            sts128(at + (((2 * q + 1) ^ (r & 7)) << 4),
+                   make_uint4(scaled2(x[2], 0x4140u, by), scaled2(x[2], 0x4342u, by), scaled2(x[3], 0x4140u, by),
+                              scaled2(x[3], 0x4342u, by)));
+          };
+          if (D == 128) {
+            // The codes lie where the upper 64 columns go, row r's in row r's place; there piece q's output covers
+            // code pieces up to q, which have been read.  A rolled loop: the softmax needs the instruction cache.
+            const uint32_t src = tile + C::HALF + r * 128;
+            uint4 c = lds128(src + ((r & 7) << 4));
+#pragma unroll 1
+            for (int q = 0; q < 8; ++q) {
+              const uint4 after = lds128(src + ((((q + 1) & 7) ^ (r & 7)) << 4));
+              widen(c, tile + (q >> 2) * C::HALF + r * 128, q & 3);
+              c = after;
+            }
+          } else {
+            // 64-byte rows over other rows' places: all are read before any is written
+            const uint32_t src = tile + C::CODES + r * 64;
             uint4 c[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) c[q] = lds128(src + (((4 * half + q) ^ sw) << 4));
-            if (D == 64) named_bar_sync(NB_CVT, 128);
-            const uint32_t at = tile + half * C::HALF + r * 128;
+            for (int q = 0; q < 4; ++q) c[q] = lds128(src + ((q ^ ((r >> 1) & 3)) << 4));
+            named_bar_sync(NB_CVT + v, 128);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t x[4] = {c[q].x ^ 0x80808080u, c[q].y ^ 0x80808080u, c[q].z ^ 0x80808080u,
-                                     c[q].w ^ 0x80808080u};
-              sts128(at + (((2 * q) ^ (r & 7)) << 4),
-                     make_uint4(scaled2(x[0], 0x4140u, by), scaled2(x[0], 0x4342u, by), scaled2(x[1], 0x4140u, by),
-                                scaled2(x[1], 0x4342u, by)));
-              sts128(at + (((2 * q + 1) ^ (r & 7)) << 4),
-                     make_uint4(scaled2(x[2], 0x4140u, by), scaled2(x[2], 0x4342u, by), scaled2(x[3], 0x4140u, by),
-                                scaled2(x[3], 0x4342u, by)));
-            }
+            for (int q = 0; q < 4; ++q) widen(c[q], tile + r * 128, q);
           }
           fence_async_shared();    // read by tcgen05.mma
           __syncwarp();
@@ -596,8 +606,6 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         const int sl = c & 1;
         const uint32_t s_c = s_addr + HN * sl;
         mbar_wait(bar(T_SFULL + 2 * t + sl), (cc >> 1) & 1, err, abort_flag);
-        const uint32_t vi = 2 * (n + (c >> 1)) + 1;   // ring position of this key tile's V
-        if (INT8 && sl == 0) mbar_wait(bar(T_FULL + vi % C::NSLOT), (vi / C::NSLOT) & 1, err, abort_flag);
         tc_fence_after();
         __syncwarp();
         float x[HN];
@@ -610,7 +618,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           for (int e = 0; e < HN; ++e) x[e] = __uint_as_float(v[e]);
         }
         if (INT8) {
-          const float* sc = scales + ((vi % C::NSLOT) >> 1) * 128 + HN * sl;
+          const float* sc = scales + ((n + (c >> 1)) % C::STAGES) * 128 + HN * sl;
 #pragma unroll
           for (int e = 0; e < HN; e += 4) {
             const float4 k4 = *reinterpret_cast<const float4*>(sc + e);
