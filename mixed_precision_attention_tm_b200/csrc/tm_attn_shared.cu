@@ -97,38 +97,43 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 }
 
 // Bytes of one 16-key stage of K (V the same), and where the 16-byte piece c
-// of key row `row` lies in it: permuted so that the reads below (ldmatrix of
-// eight rows; for INT8, 16-byte reads of two rows' quarters for K and of four
-// even or odd rows for V) meet no bank twice.
+// of key row `row` lies in it: as the TMA copy of 16 rows writes it, 64
+// columns (fp16) at a time in the 128-byte swizzle, INT8 rows of 64 bytes in the
+// 64-byte one.  The reads below (ldmatrix of eight rows; 16-byte reads of
+// codes) meet banks at most twice.
 template <int D, bool INT8>
 struct Stage {
   static constexpr int ROW = D * (INT8 ? 1 : 2);
   static constexpr int BYTES = kStep * ROW;
   static constexpr int PIECES = ROW / 16;
-  __device__ static __forceinline__ uint32_t at(int row, int c, bool is_v) {
-    if (!INT8) return row * ROW + ((c ^ (row & 7)) << 4);
-    if (D == 128) return row * ROW + ((c ^ (is_v ? ((row >> 1) & 3) << 1 : (row & 1) << 2)) << 4);
-    const int line = row >> 1, i = ((row & 1) << 2) | c;
-    return line * 128 + ((i ^ ((line & 3) << 1)) << 4);
+  __device__ static __forceinline__ uint32_t at(int row, int c) {
+    if (INT8 && D == 64) return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+    return (c >> 3) * (kStep * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
   }
 };
 
 template <int D, bool INT8>
-constexpr int split_smem() {
-  return kWarps * (kStages * (2 * Stage<D, INT8>::BYTES + (INT8 ? 3 * kStep * 4 : 0)) + 16 * 8);
-}
+struct SplitSmem {
+  static constexpr int RING = kWarps * kStages * 2 * Stage<D, INT8>::BYTES;
+  static constexpr int OFF_SCALE = RING;                                              // [warp][stage][3][16] floats
+  static constexpr int OFF_ML = OFF_SCALE + (INT8 ? kWarps * kStages * 3 * kStep * 4 : 0);   // [warp][16] (m, l)
+  static constexpr int OFF_BAR = OFF_ML + kWarps * 16 * 8;                            // [warp][stage], abort flag
+  static constexpr int BYTES = OFF_BAR + kWarps * kStages * 8 + 16 + 1024;
+};
 
 // Attention of up to 16 packed rows over one range of keys.
 //
 // Decoding reads far more than it computes (a key's 2 d values serve g rows),
 // so this is built around the copies: each warp owns every fourth 16-key step
-// and its own three-stage ring of cp.async copies, with no barrier between
-// warps until the join at the end.  A warp's step is a chain of dependent
+// and its own three-stage ring, with no barrier between warps until the join at
+// the end.  A warp's step is a chain of dependent
 // instructions, so it takes several warps to keep up with the copies: at
 // d = 128 in fp16 two CTAs (eight warps, 192 KB of rings) fit an SM, else
 // more.  With two warps of 32-key steps per CTA the same batch (64 sequences of 64 to
-// 1024 tokens, 143 MB) took 43 us.  A step's keys lie in one page, so its copies need one
-// block-table entry.  Rows past the range's end are filled with zeros and
+// 1024 tokens, 143 MB) took 43 us.  A step's keys lie in one page, so a TMA copy
+// brings its K (two at d = 128 in fp16), another its V, for a dozen
+// instructions where row copies took over a hundred.  A step that the range
+// ends in, or on a bad page, is copied row by row: rows past the end are zeros and
 // never read from memory.  The products run on mma.sync m16n8k16: 16 rows
 // hold a whole group of query heads, where a 128-row tensor-memory tile would
 // be nearly empty.
@@ -141,70 +146,71 @@ constexpr int split_smem() {
 // lane's 16 consecutive codes serve four MMAs; the order of output columns is
 // free too, so a lane's n index stands for d / 8 consecutive dimensions.
 template <int D, bool INT8>
-__device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
+__device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& maps, DevErr err) {
   using S = Stage<D, INT8>;
+  using L_ = SplitSmem<D, INT8>;
   constexpr int NT = D / 8, KS = D / 16;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane & 3, r8 = lane >> 2;
   const SharedPlan& p = a.plan;
   const int H = a.pool.H, g = p.group, Hq = H * g;
 
-  // ---- which rows and keys
-  int64_t item = blockIdx.x;
-  const int kvh = static_cast<int>(item % H);
+  // ---- which rows and keys (packed rows and keys stay below 2^31)
+  int item = blockIdx.x;
+  const int kvh = item % H;
   item /= H;
-  const int64_t pre_items = p.pre_tile ? 0 : static_cast<int64_t>(p.pre_splits) * p.pre_rows;
+  const int pre_items = p.pre_tile ? 0 : p.pre_splits * p.pre_rows;
   const bool prefix = item < pre_items;
-  int b = 0, slot;
-  int64_t row0, start = 0, nrows, k0, k1, hidden = 0;   // hidden: own keys that row 0's token does not see
-  int64_t lk = 0;
+  int b = 0, slot, row0, start = 0, nrows, k0, k1;
+  int hidden = 0;         // own, causal: token i of the sequence sees keys below hidden + i
   if (prefix) {
-    row0 = (item % p.pre_rows) * 16;
-    slot = static_cast<int>(item / p.pre_rows);
-    nrows = a.T * g;
-    k0 = static_cast<int64_t>(slot) * p.pre_chunk;
-    k1 = k0 + p.pre_chunk < a.prefix_len ? k0 + p.pre_chunk : a.prefix_len;
-    lk = a.prefix_len;
+    slot = item / p.pre_rows;
+    row0 = (item - slot * p.pre_rows) * 16;
+    nrows = static_cast<int>(a.T) * g;
+    k0 = slot * p.pre_chunk;
+    k1 = min(k0 + p.pre_chunk, static_cast<int>(a.prefix_len));
   } else {
     item -= pre_items;
-    const int64_t per = static_cast<int64_t>(a.batch) * p.own_rows;
-    const int split = static_cast<int>(item / per);
-    item %= per;
-    b = static_cast<int>(item / p.own_rows);
-    row0 = (item % p.own_rows) * 16;
+    const int per = a.batch * p.own_rows;
+    const int split = item / per;
+    item -= split * per;
+    b = item / p.own_rows;
+    row0 = (item - b * p.own_rows) * 16;
     slot = p.pre_splits + split;
-    int64_t n;
-    seq_rows(a, b, start, n);
-    nrows = n * g;
-    const bool outside = start < 0 || start + n > a.T || nrows > static_cast<int64_t>(p.own_rows) * 16;
+    int64_t start64, n64;
+    seq_rows(a, b, start64, n64);
+    const bool outside = start64 < 0 || n64 < 0 || start64 + n64 > a.T || n64 * g > static_cast<int64_t>(p.own_rows) * 16;
     if (outside && threadIdx.x == 0) dev_error(err, TM_DEVERR_SEQLEN);   // offsets that the launch was not sized for
-    if (outside || row0 >= nrows) return;
-    lk = __ldg(a.kv_lens + b);
+    const int n = static_cast<int>(n64);
+    if (outside || row0 >= n * g) return;
+    start = static_cast<int>(start64);
+    nrows = n * g;
+    int lk = __ldg(a.kv_lens + b);
     if (lk > a.max_kv) {
       if (threadIdx.x == 0) dev_error(err, TM_DEVERR_SEQLEN);
-      lk = a.max_kv;
+      lk = static_cast<int>(a.max_kv);
     }
-    if (lk < 0) lk = 0;
-    const int64_t last = (row0 + 16 < nrows ? row0 + 16 : nrows) - 1;
-    const int64_t seen = a.causal ? last / g + lk - n + 1 : lk;   // keys the block's last row sees
-    k0 = static_cast<int64_t>(split) * p.own_chunk;
-    k1 = k0 + p.own_chunk < lk ? k0 + p.own_chunk : lk;
-    if (k1 > seen) k1 = seen;
-    hidden = a.causal ? lk - n + 1 : lk;    // token i of the sequence sees keys below hidden + i (causal)
+    lk = max(lk, 0);
+    hidden = lk - n + 1;
+    k0 = split * p.own_chunk;
+    k1 = min(k0 + p.own_chunk, lk);
+    if (a.causal) k1 = min(k1, hidden + (min(row0 + 16, nrows) - 1) / g);   // keys that the block's last row sees
   }
-  const int rows = static_cast<int>(nrows - row0 < 16 ? nrows - row0 : 16);
-  const int64_t total = static_cast<int64_t>(a.T) * Hq;
+  const int rows = min(nrows - row0, 16);
+  const int64_t total = a.T * Hq;
   const bool direct = p.slots == 1;
 
   // (token, query head) of packed row r of this block
   auto token_of = [&](int r) { return start + (row0 + r) / g; };
-  auto head_of = [&](int r) { return kvh * g + static_cast<int>((row0 + r) % g); };
+  auto head_of = [&](int r) { return kvh * g + (row0 + r) % g; };
 
   if (k0 >= k1) {     // nothing visible here
     if (!direct) {
       if (threadIdx.x < rows)
-        a.ml[slot * total + token_of(threadIdx.x) * Hq + head_of(threadIdx.x)] = make_float2(-INFINITY, 0.f);
+        a.ml[slot * total + static_cast<int64_t>(token_of(threadIdx.x)) * Hq + head_of(threadIdx.x)] =
+            make_float2(-INFINITY, 0.f);
     } else {
       for (int i = threadIdx.x; i < rows * (D / 8); i += kWarps * 32) {
         const int r = i / (D / 8);
@@ -216,23 +222,100 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
     return;
   }
 
-  // ---- this lane's rows r8 and r8 + 8: limits and Q fragments
-  int64_t lim[2];
+  uint8_t* ring = smem + warp * kStages * 2 * S::BYTES;
+  const uint32_t ring_s = smem_u32(ring);
+  float* scales = reinterpret_cast<float*>(smem + L_::OFF_SCALE) + warp * kStages * 3 * kStep;
+  float2* ml_s = reinterpret_cast<float2*>(smem + L_::OFF_ML);
+  const uint32_t bar0 = smem_u32(smem + L_::OFF_BAR) + warp * kStages * 8;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L_::OFF_BAR + kWarps * kStages * 8);
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(bar0 + 8 * i, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncwarp();
+
+  const int first = k0 + warp * kStep;
+  const int steps = first < k1 ? (k1 - first + kWarps * kStep - 1) / (kWarps * kStep) : 0;
+  const int shift = a.pool.page_shift, page_mask = (1 << shift) - 1;
+
+  // page of step i as the table has it; -1 where nothing is to be read
+  auto entry_at = [&](int i) -> int32_t {
+    if (i >= steps) return -1;
+    const int col = (first + i * (kWarps * kStep)) >> shift;
+    if (!prefix && col >= a.pt.cols) return -1;
+    return __ldg(prefix ? a.prefix_pages + col : a.pt.table + b * a.pt.stride + col);
+  };
+  float pend_k = 0.f, pend_v = 1.f;
+  uint32_t by_tma = 0;      // bit s: stage s is filled by TMA
+  // copies of step i into stage st; the scales follow one call later
+  auto issue = [&](int i, int st, int32_t page) {
+    if (INT8 && i > 0 && lane < kStep) {
+      float* sc = scales + (st == 0 ? kStages - 1 : st - 1) * 3 * kStep + lane;
+      const float f = pend_v == 0.f ? 5.9604645e-8f : pend_v;   // a zero scale (codes all 0) counts in the row sum alone
+      sc[0] = pend_k * a.scale_log2;
+      sc[kStep] = log2f(f);
+      sc[2 * kStep] = 1.0f / f;
+    }
+    if (i < steps) {
+      const int key = first + i * (kWarps * kStep), s = key & page_mask;
+      const bool ok = page_ok(page, a.pool.num_pages);
+      if (!ok && lane == 0) dev_error(err, TM_DEVERR_SEQLEN);
+      const int valid = ok ? min(k1 - key, kStep) : 0;
+      if (INT8) {
+        const int64_t so = page * a.pool.sstride_page + (s + lane) * a.pool.sstride_t + kvh * a.pool.sstride_h;
+        pend_k = lane < valid ? __half2float(a.pool.ks[so]) : 0.f;
+        pend_v = lane < valid ? __half2float(a.pool.vs[so]) : 0.f;
+      }
+      const uint32_t dst = ring_s + st * 2 * S::BYTES;
+      if (maps.ok && valid == kStep) {
+        by_tma |= 1u << st;
+        if (elect_one()) {
+          const uint32_t bar = bar0 + 8 * st;
+          mbar_arrive_expect_tx(bar, 2 * S::BYTES);
+          const int32_t c1 = maps.heads_inner ? kvh : s, c2 = maps.heads_inner ? s : kvh;
+#pragma unroll
+          for (int hh = 0; hh < (INT8 ? 1 : D / 64); ++hh) {
+            tma_load_4d(dst + hh * kStep * 128, &maps.k, bar, hh * 64, c1, c2, page);
+            tma_load_4d(dst + S::BYTES + hh * kStep * 128, &maps.v, bar, hh * 64, c1, c2, page);
+          }
+        }
+        __syncwarp();
+      } else {
+        by_tma &= ~(1u << st);
+        constexpr int RPI = 32 / S::PIECES;          // rows of one copy instruction
+        const int c = lane % S::PIECES;
+        const int64_t off = (valid > 0 ? page * a.pool.stride_page + s * a.pool.stride_t : 0) + kvh * a.pool.stride_h + c * 16;
+#pragma unroll 1
+        for (int row = lane / S::PIECES; row < kStep; row += RPI) {
+          const bool real = row < valid;
+          const int64_t at = real ? off + row * a.pool.stride_t : 0;
+          cp16(dst + S::at(row, c), a.pool.k + at, real);
+          cp16(dst + S::BYTES + S::at(row, c), a.pool.v + at, real);
+        }
+      }
+    }
+    cp_commit();
+  };
+  int32_t page = entry_at(0), page1 = entry_at(1);
+  issue(0, 0, page);
+  page = entry_at(2);
+  issue(1, 1, page1);
+
+  // ---- this lane's rows r8 and r8 + 8: limits and Q fragments, while the first copies are under way
+  int lim[2];
   uint32_t qf[KS][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = r8 + 8 * i;
     const bool real = r < rows;
-    lim[i] = lk;
-    if (!prefix && a.causal && real) {
-      const int64_t l = hidden + (row0 + r) / g;
-      lim[i] = l < lk ? l : lk;
-    }
+    lim[i] = k1;
+    if (!prefix && a.causal && real) lim[i] = min(k1, hidden + (row0 + r) / g);
     const __half* q = real ? a.q + token_of(r) * a.q_t + head_of(r) * a.q_h : a.q;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       if (INT8) {
-        // k-step s: codes (D / 4) * (s / 4 ...): lane's 16-byte piece s / 4 (d = 128: at 64 (s / 4) + 16 quad), word s % 4
+        // k-step s takes word s % 4 of the lane's 16-byte piece at 64 (s / 4) + 16 quad
         const int at = (s >> 2) * 64 + quad * 16 + (s & 3) * 4;
         const uint2 v = real ? *reinterpret_cast<const uint2*>(q + at) : make_uint2(0, 0);
         qf[s][i] = v.x;
@@ -244,92 +327,30 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
     }
   }
   // steps that end at or below this key need no mask
-  int64_t open = k1;
-  if (!prefix && a.causal) {
-    const int64_t l = hidden + row0 / g;
-    if (l < open) open = l;
-  }
-
-  uint8_t* ring = smem + warp * kStages * 2 * S::BYTES;
-  const uint32_t ring_s = smem_u32(ring);
-  float* scales = reinterpret_cast<float*>(smem + kWarps * kStages * 2 * S::BYTES) + warp * kStages * 3 * kStep;
-  float2* ml_s = reinterpret_cast<float2*>(smem + kWarps * kStages * (2 * S::BYTES + (INT8 ? 3 * kStep * 4 : 0)));
-
-  const uint8_t* kbase = a.pool.k + kvh * a.pool.stride_h;
-  const uint8_t* vbase = a.pool.v + kvh * a.pool.stride_h;
-  const int64_t first = k0 + warp * kStep;
-  const int steps = first < k1 ? static_cast<int>((k1 - first + kWarps * kStep - 1) / (kWarps * kStep)) : 0;
-  const int shift = a.pool.page_shift;
-
-  // page of step i, -1 where nothing is to be read
-  auto page_at = [&](int i) -> int32_t {
-    if (i >= steps) return -1;
-    const int64_t key = first + static_cast<int64_t>(i) * (kWarps * kStep);
-    int32_t page;
-    if (prefix) {
-      page = __ldg(a.prefix_pages + (key >> shift));
-      if (!page_ok(page, a.pool.num_pages)) page = -1;
-    } else {
-      page = page_of(a.pt, b, key);
-    }
-    if (page < 0 && lane == 0) dev_error(err, TM_DEVERR_SEQLEN);
-    return page;
-  };
-  constexpr int RPI = 32 / S::PIECES;          // rows of one copy instruction
-  const int cp_c = lane % S::PIECES, cp_r = lane / S::PIECES;
-  const int64_t cp_off = cp_r * a.pool.stride_t + cp_c * 16;
-  float pend_k = 0.f, pend_v = 1.f;
-  // copies of step i into its stage; the scales follow one call later
-  auto issue = [&](int i, int32_t page) {
-    if (INT8 && i > 0 && lane < kStep) {
-      float* sc = scales + (i - 1) % kStages * 3 * kStep + lane;
-      const float f = pend_v == 0.f ? 5.9604645e-8f : pend_v;   // a zero scale (codes all 0) counts in the row sum alone
-      sc[0] = pend_k * a.scale_log2;
-      sc[kStep] = log2f(f);
-      sc[2 * kStep] = 1.0f / f;
-    }
-    if (i < steps) {
-      const int64_t key = first + static_cast<int64_t>(i) * (kWarps * kStep);
-      const int64_t s = key & ((1 << shift) - 1);
-      const int valid = page >= 0 ? static_cast<int>(k1 - key < kStep ? k1 - key : kStep) : 0;
-      const int64_t off = valid > 0 ? page * a.pool.stride_page + s * a.pool.stride_t : 0;
-      if (INT8) {
-        const int64_t so = page * a.pool.sstride_page + (s + lane) * a.pool.sstride_t + kvh * a.pool.sstride_h;
-        pend_k = lane < valid ? __half2float(a.pool.ks[so]) : 0.f;
-        pend_v = lane < valid ? __half2float(a.pool.vs[so]) : 0.f;
-      }
-      const uint32_t dst = ring_s + (i % kStages) * 2 * S::BYTES;
-#pragma unroll
-      for (int n = 0; n < kStep / RPI; ++n) {
-        const int row = n * RPI + cp_r;
-        const bool real = row < valid;
-        const int64_t at = real ? off + cp_off + n * RPI * a.pool.stride_t : 0;
-        cp16(dst + S::at(row, cp_c, false), kbase + at, real);
-        cp16(dst + S::BYTES + S::at(row, cp_c, true), vbase + at, real);
-      }
-    }
-    cp_commit();
-  };
+  int open = k1;
+  if (!prefix && a.causal) open = min(open, hidden + row0 / g);
 
   float o[NT][4];
 #pragma unroll
   for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-  int32_t page = page_at(0), page1 = page_at(1);
-  issue(0, page);
-  page = page_at(2);
-  issue(1, page1);
-
+  int st = 0;
+  uint32_t laps = 0;        // bit s: parity of stage s's next TMA fill
   for (int i = 0; i < steps; ++i) {
-    cp_wait<1>();
+    cp_wait<1>();           // this step's row copies, if any
+    if (by_tma >> st & 1) {
+      mbar_wait(bar0 + 8 * st, laps >> st & 1, err, abort_flag);
+      laps ^= 1u << st;
+    }
     __syncwarp();
-    issue(i + 2, page);      // into the stage that step i - 1 used
-    page = page_at(i + 3);
-    const uint32_t ks_s = ring_s + (i % kStages) * 2 * S::BYTES;
+    issue(i + 2, st == 0 ? kStages - 1 : st - 1, page);      // into the stage that step i - 1 used
+    page = entry_at(i + 3);
+    const uint32_t ks_s = ring_s + st * 2 * S::BYTES;
     const uint32_t vs_s = ks_s + S::BYTES;
-    const float* sc = scales + (i % kStages) * 3 * kStep + 2 * quad;
-    const int64_t key0 = first + static_cast<int64_t>(i) * (kWarps * kStep);
+    const float* sc = scales + st * 3 * kStep + 2 * quad;
+    const int key0 = first + i * (kWarps * kStep);
+    st = st == kStages - 1 ? 0 : st + 1;
 
     // even and odd halves of d in sums of their own: half the chain of dependent MMAs
     float s[2][4], s2[2][4];
@@ -344,7 +365,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           uint32_t bfr[4];
-          ldsm4(ks_s + S::at(8 * j + (lane & 7), 2 * ks + (lane >> 3), false), bfr);
+          ldsm4(ks_s + S::at(8 * j + (lane & 7), 2 * ks + (lane >> 3)), bfr);
           mma16816(s[j], qf[ks], bfr[0], bfr[1]);
           mma16816(s2[j], qf[ks + 1], bfr[2], bfr[3]);
         }
@@ -354,7 +375,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
       for (int c = 0; c < KS / 4; ++c) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint4 v = lds128(ks_s + S::at(8 * j + r8, 4 * c + quad, false));
+          const uint4 v = lds128(ks_s + S::at(8 * j + r8, 4 * c + quad));
           const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -389,8 +410,8 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int64_t key = key0 + 8 * j + 2 * quad + (e & 1);
-          if (key >= k1 || key >= lim[e >> 1]) x[j][e] = -INFINITY;
+          const int key = key0 + 8 * j + 2 * quad + (e & 1);
+          if (key >= lim[e >> 1]) x[j][e] = -INFINITY;
         }
       }
     }
@@ -438,7 +459,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
 #pragma unroll
       for (int n = 0; n < NT; n += 2) {
         uint32_t bfr[4];
-        ldsm4t(vs_s + S::at(((lane >> 3) & 1) * 8 + (lane & 7), n + (lane >> 4), true), bfr);
+        ldsm4t(vs_s + S::at(((lane >> 3) & 1) * 8 + (lane & 7), n + (lane >> 4)), bfr);
         mma16816(o[n], pf, bfr[0], bfr[1]);
         mma16816(o[n + 1], pf, bfr[2], bfr[3]);
       }
@@ -450,13 +471,13 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
       for (int e = 0; e < 4; ++e) {
         const int row = 2 * quad + (e & 1) + 8 * (e >> 1);
         if (D == 128) {
-          const uint4 v = lds128(vs_s + S::at(row, r8, true));
+          const uint4 v = lds128(vs_s + S::at(row, r8));
           w[e][0] = v.x ^ 0x80808080u;
           w[e][1] = v.y ^ 0x80808080u;
           w[e][D / 32 - 2] = v.z ^ 0x80808080u;
           w[e][D / 32 - 1] = v.w ^ 0x80808080u;
         } else {
-          const uint2 v = lds64(vs_s + S::at(row, r8 >> 1, true) + (r8 & 1) * 8);
+          const uint2 v = lds64(vs_s + S::at(row, r8 >> 1) + (r8 & 1) * 8);
           w[e][0] = v.x ^ 0x80808080u;
           w[e][1] = v.y ^ 0x80808080u;
         }
@@ -565,9 +586,10 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, DevErr err) {
 }
 
 template <int D, bool INT8>
-__global__ void __launch_bounds__(kWarps * 32) split_kernel(const __grid_constant__ SharedArgs a, DevErr err) {
+__global__ void __launch_bounds__(kWarps * 32)
+    split_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ PageMaps maps, DevErr err) {
   pdl_launch_dependents();
-  split_rows<D, INT8>(a, err);
+  split_rows<D, INT8>(a, maps, err);
   pdl_wait();      // whoever waits for this kernel has waited for the one before it
 }
 
@@ -751,14 +773,15 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Share
 
 template <int D, bool INT8>
 tm_status launch_split(const SharedArgs& a, bool overlap, DevErr err, cudaStream_t stream) {
-  constexpr int smem = split_smem<D, INT8>();
+  constexpr int smem = SplitSmem<D, INT8>::BYTES;
   static std::atomic<uint64_t> prepared{0};
   const tm_status st = prepare_smem(split_kernel<D, INT8>, smem, prepared);
   if (st != TM_OK) return st;
   const SharedPlan& p = a.plan;
   const int64_t items = ((p.pre_tile ? 0 : static_cast<int64_t>(p.pre_splits) * p.pre_rows) +
                          (p.own_tile ? 0 : static_cast<int64_t>(p.own_splits) * a.batch * p.own_rows)) * a.pool.H;
-  return launch_kernel(split_kernel<D, INT8>, items, kWarps * 32, smem, overlap, stream, a, err);
+  return launch_kernel(split_kernel<D, INT8>, items, kWarps * 32, smem, overlap, stream, a,
+                       page_maps(a.pool, D, INT8, kStep), err);
 }
 
 // Up to three kernels, each allowed to start while the one before it drains:

@@ -143,6 +143,15 @@ tm_status launch_kernel(void (*kernel)(P...), int64_t blocks, int threads, int s
   return check_cuda(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
+// TMA maps of a page pool, [page][slot or head][head or slot][d], for copies of
+// `rows` slots of one head (64 columns of fp16, whole rows of codes).
+struct PageMaps {
+  CUtensorMap k, v;
+  int ok;             // 0 where the driver has no map for the layout: rows are copied one by one
+  int heads_inner;    // order of the middle dimensions: (heads, slots) or (slots, heads)
+};
+PageMaps page_maps(const PagedPool& pool, int d, bool int8, int rows);
+
 // tm_attn_shared_tile.cu: the prefix's (or the own tokens') part on the tile kernel.
 tm_status shared_tile(const SharedArgs& a, int d, bool int8, bool prefix, bool overlap, DevErr err,
                       cudaStream_t stream);

@@ -125,19 +125,18 @@ __device__ __forceinline__ void exp2_fma2(uint64_t y2, float& p0, float& p1) {
   p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
 }
 
-struct TileMaps {
-  CUtensorMap q, k, v;
-  int q_tma;          // Q through its map: 128 rows are whole tokens
-  int kv_tma;         // K and V through theirs
-  int heads_inner;    // order of the page maps' middle dimensions: (heads, slots) or (slots, heads)
-};
-
 // codes2 times a scale: a code and a product's one rounding
 __device__ __forceinline__ uint32_t scaled2(uint32_t w, uint32_t sel, __half2 by) {
   const uint32_t c = codes2(w, sel);
   const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&c), by);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+
+struct TileMaps {
+  CUtensorMap q;
+  int q_tma;          // Q through its map: 128 rows are whole tokens
+  PageMaps kv;
+};
 
 template <int D, bool INT8>
 __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
@@ -347,7 +346,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         __syncwarp();
         if (lane < boxes) {
           const int32_t s0 = key & page_mask;
-          const int32_t c1 = maps.heads_inner ? sg.kvh : s0, c2 = maps.heads_inner ? s0 : sg.kvh;
+          const int32_t c1 = maps.kv.heads_inner ? sg.kvh : s0, c2 = maps.kv.heads_inner ? s0 : sg.kvh;
 #pragma unroll
           for (int hh = 0; hh < (INT8 ? 1 : D / 64); ++hh)
             tma_load_4d(tile + hh * C::HALF + (lane << box_shift) * (INT8 ? D : 128), map, bar(LANDED + slot), hh * 64,
@@ -431,12 +430,12 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           const int32_t next = my_page(j + 1);
           if (page == -2) dev_error(err, TM_DEVERR_SEQLEN);
           const uint32_t i = 2 * n;
-          if (maps.kv_tma && key0 + 128 <= sg.lk && __all_sync(0xffffffffu, lane >= boxes || page >= 0)) {
+          if (maps.kv.ok && key0 + 128 <= sg.lk && __all_sync(0xffffffffu, lane >= boxes || page >= 0)) {
             const int key = key0 + lane * step;
             acquire(i);
-            copy_boxes(&maps.k, i % C::NSLOT, page, key);
+            copy_boxes(&maps.kv.k, i % C::NSLOT, page, key);
             acquire(i + 1);
-            copy_boxes(&maps.v, (i + 1) % C::NSLOT, page, key);
+            copy_boxes(&maps.kv.v, (i + 1) % C::NSLOT, page, key);
           } else {
             const int32_t run_page = __shfl_sync(0xffffffffu, page, ((lane & 7) * 16) >> box_shift);
             acquire(i);
@@ -765,6 +764,22 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
 
 }  // namespace
 
+PageMaps page_maps(const PagedPool& pool, int d, bool int8, int rows) {
+  PageMaps m{};
+  m.heads_inner = pool.stride_h < pool.stride_t;
+  const int64_t page_size = 1ll << pool.page_shift;
+  const int box_rows = page_size < rows ? static_cast<int>(page_size) : rows;
+  const int64_t dims[4] = {d, m.heads_inner ? pool.H : page_size, m.heads_inner ? page_size : pool.H, pool.num_pages};
+  const int64_t strides[3] = {m.heads_inner ? pool.stride_h : pool.stride_t, m.heads_inner ? pool.stride_t : pool.stride_h,
+                              pool.stride_page};
+  const int box[4] = {int8 ? d : 64, m.heads_inner ? 1 : box_rows, m.heads_inner ? box_rows : 1, 1};
+  const CUtensorMapDataType type = int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUtensorMapSwizzle swz = int8 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  m.ok = encode_tiled_map(&m.k, pool.k, type, 4, dims, strides, box, swz) &&
+         encode_tiled_map(&m.v, pool.v, type, 4, dims, strides, box, swz);
+  return m;
+}
+
 template <int D, bool INT8>
 static tm_status launch_tile(const SharedArgs& a, bool prefix, bool overlap, DevErr err, cudaStream_t stream) {
   using C = CfgT<D, INT8>;
@@ -772,23 +787,9 @@ static tm_status launch_tile(const SharedArgs& a, bool prefix, bool overlap, Dev
   tm_status st = prepare_smem(tile_kernel<D, INT8>, C::SMEM, prepared);
   if (st != TM_OK) return st;
   const SharedPlan& p = a.plan;
-  const PagedPool& pool = a.pool;
   TileMaps m{};
-  const int g = p.group, Hq = pool.H * g;
-  const int64_t box_rows = pool.page_shift < 7 ? 1 << pool.page_shift : 128;
-  // pages as a tensor [page][slot or head][head or slot][d]
-  m.heads_inner = pool.stride_h < pool.stride_t;
-  const int64_t page_size = 1ll << pool.page_shift;
-  const int64_t dims[4] = {D, m.heads_inner ? pool.H : page_size, m.heads_inner ? page_size : pool.H, pool.num_pages};
-  const int64_t strides[3] = {m.heads_inner ? pool.stride_h : pool.stride_t, m.heads_inner ? pool.stride_t : pool.stride_h,
-                              pool.stride_page};
-  const int box[4] = {INT8 ? D : 64, static_cast<int>(m.heads_inner ? 1 : box_rows),
-                      static_cast<int>(m.heads_inner ? box_rows : 1), 1};
-  const CUtensorMapDataType type = INT8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const CUtensorMapSwizzle swz = INT8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-  // where the driver has no map for a layout, rows are copied one by one
-  m.kv_tma = encode_tiled_map(&m.k, pool.k, type, 4, dims, strides, box, swz) &&
-             encode_tiled_map(&m.v, pool.v, type, 4, dims, strides, box, swz);
+  const int g = p.group, Hq = a.pool.H * g;
+  m.kv = page_maps(a.pool, D, INT8, 128);
   if (128 % g == 0) {
     const int64_t qdims[3] = {D, Hq, a.T};
     const int64_t qstrides[2] = {(Hq > 1 ? a.q_h : D) * 2, (a.T > 1 ? a.q_t : D * Hq) * 2};
@@ -796,7 +797,7 @@ static tm_status launch_tile(const SharedArgs& a, bool prefix, bool overlap, Dev
     m.q_tma = encode_tiled_map(&m.q, a.q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, qdims, qstrides, qbox,
                                CU_TENSOR_MAP_SWIZZLE_128B);
   }
-  const int64_t items = prefix ? p.pre_ctas : static_cast<int64_t>(p.own_splits) * a.batch * p.own_rows * pool.H;
+  const int64_t items = prefix ? p.pre_ctas : static_cast<int64_t>(p.own_splits) * a.batch * p.own_rows * a.pool.H;
   return launch_kernel(tile_kernel<D, INT8>, items, C::THREADS, C::SMEM, overlap, stream, a, m, prefix ? 1 : 0, err);
 }
 
