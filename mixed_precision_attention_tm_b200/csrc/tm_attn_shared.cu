@@ -23,27 +23,44 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t ba
   const int64_t own_units = ceil_div(max_kv_len, 128), pre_units = ceil_div(prefix_len, 128);
   p.own_rows = static_cast<int>(own_rows);
   p.pre_rows = static_cast<int>(pre_rows);
-  // split kernel: pieces small enough for eight CTAs per SM, so that sequences of different lengths (known on the
+  // split kernel: pieces small enough for five CTAs per SM, so that sequences of different lengths (known on the
   // device alone) even out over the SMs; at most kMostSplits of each
   const int64_t split_units = (p.own_tile ? 0 : batch * own_rows * Hkv * own_units) +
                               (p.pre_tile ? 0 : pre_rows * Hkv * pre_units);
-  int64_t chunk = ceil_div(split_units, 8 * kSmsB200);
+  int64_t chunk = ceil_div(split_units, 5 * kSmsB200);
   if (chunk < 1) chunk = 1;
   if (p.pre_tile) {
-    // equal pieces of the line of key tiles, one for each SM
-    const int64_t line = Hkv * pre_rows * pre_units;
+    // Equal pieces of the line of key tiles, one for each SM; or, where that costs a CTA at most kSplitBlockTiles more
+    // key tiles, equal pieces of every row block, so that no CTA pays a second block's start and end.
+    const int64_t blocks = Hkv * pre_rows, line = blocks * pre_units;
     if (line >= (1ll << 31)) {
       p.bytes = -1;
       return p;
     }
+    const int64_t least = ceil_div(pre_units, kMostSplits);
     int64_t c = ceil_div(line, kSmsB200);
-    if (c < ceil_div(pre_units, kMostSplits)) c = ceil_div(pre_units, kMostSplits);
-    if (c > line) c = line;
+    if (blocks <= kSmsB200) {
+      const int64_t whole = ceil_div(pre_units, kSmsB200 / blocks);
+      if (whole <= c + kSplitBlockTiles) {
+        c = whole;
+        p.pre_pieces = 1;
+      }
+    }
+    if (c < least) c = least;
     if (c < 1) c = 1;
     p.pre_tiles = static_cast<int>(pre_units);
-    p.pre_chunk = static_cast<int>(c);
-    p.pre_ctas = static_cast<int>(ceil_div(line, c));
-    p.pre_splits = static_cast<int>(line <= c ? 1 : (pre_units % c == 0 ? pre_units / c : ceil_div(pre_units - 1, c) + 1));
+    if (p.pre_pieces != 0) {
+      p.pre_pieces = static_cast<int>(ceil_div(pre_units, c));
+      p.pre_chunk = static_cast<int>(ceil_div(pre_units, p.pre_pieces));
+      p.pre_pieces = static_cast<int>(ceil_div(pre_units, p.pre_chunk));
+      p.pre_ctas = static_cast<int>(blocks * p.pre_pieces);
+      p.pre_splits = p.pre_pieces;
+    } else {
+      if (c > line) c = line;
+      p.pre_chunk = static_cast<int>(c);
+      p.pre_ctas = static_cast<int>(ceil_div(line, c));
+      p.pre_splits = static_cast<int>(line <= c ? 1 : (pre_units % c == 0 ? pre_units / c : ceil_div(pre_units - 1, c) + 1));
+    }
   } else {
     const int64_t c = chunk > ceil_div(pre_units, kMostSplits) ? chunk : ceil_div(pre_units, kMostSplits);
     p.pre_chunk = static_cast<int>((c < 1 ? 1 : c) * 128);
@@ -179,6 +196,19 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
     b = item / p.own_rows;
     row0 = (item - b * p.own_rows) * 16;
     slot = p.pre_splits + split;
+    k0 = split * p.own_chunk;
+  }
+  // the first steps' table entries, before the lengths are known: one latency less
+  const int shift = a.pool.page_shift, page_mask = (1 << shift) - 1;
+  const int first = k0 + warp * kStep;
+  const int key_bound = prefix ? static_cast<int>(a.prefix_len) : static_cast<int>(a.max_kv);
+  auto raw_entry = [&](int key) -> int32_t {
+    const int col = key >> shift;
+    if (key >= key_bound || (!prefix && col >= a.pt.cols)) return -1;
+    return __ldg(prefix ? a.prefix_pages + col : a.pt.table + b * a.pt.stride + col);
+  };
+  int32_t page = raw_entry(first), page1 = raw_entry(first + kWarps * kStep), page2 = raw_entry(first + 2 * kWarps * kStep);
+  if (!prefix) {
     int64_t start64, n64;
     seq_rows(a, b, start64, n64);
     const bool outside = start64 < 0 || n64 < 0 || start64 + n64 > a.T || n64 * g > static_cast<int64_t>(p.own_rows) * 16;
@@ -194,7 +224,6 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
     }
     lk = max(lk, 0);
     hidden = lk - n + 1;
-    k0 = split * p.own_chunk;
     k1 = min(k0 + p.own_chunk, lk);
     if (a.causal) k1 = min(k1, hidden + (min(row0 + 16, nrows) - 1) / g);   // keys that the block's last row sees
   }
@@ -235,28 +264,24 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
   }
   __syncwarp();
 
-  const int first = k0 + warp * kStep;
   const int steps = first < k1 ? (k1 - first + kWarps * kStep - 1) / (kWarps * kStep) : 0;
-  const int shift = a.pool.page_shift, page_mask = (1 << shift) - 1;
-
   // page of step i as the table has it; -1 where nothing is to be read
-  auto entry_at = [&](int i) -> int32_t {
-    if (i >= steps) return -1;
-    const int col = (first + i * (kWarps * kStep)) >> shift;
-    if (!prefix && col >= a.pt.cols) return -1;
-    return __ldg(prefix ? a.prefix_pages + col : a.pt.table + b * a.pt.stride + col);
-  };
-  float pend_k = 0.f, pend_v = 1.f;
+  auto entry_at = [&](int i) -> int32_t { return i < steps ? raw_entry(first + i * (kWarps * kStep)) : -1; };
   uint32_t by_tma = 0;      // bit s: stage s is filled by TMA
-  // copies of step i into stage st; the scales follow one call later
-  auto issue = [&](int i, int st, int32_t page) {
-    if (INT8 && i > 0 && lane < kStep) {
-      float* sc = scales + (st == 0 ? kStages - 1 : st - 1) * 3 * kStep + lane;
-      const float f = pend_v == 0.f ? 5.9604645e-8f : pend_v;   // a zero scale (codes all 0) counts in the row sum alone
-      sc[0] = pend_k * a.scale_log2;
-      sc[kStep] = log2f(f);
-      sc[2 * kStep] = 1.0f / f;
-    }
+  struct Scales {
+    float k, v;
+  };
+  // INT8: a step's scales, as issue() loaded them, into its stage
+  auto keep_scales = [&](int st, const Scales& x) {
+    if (!INT8 || lane >= kStep) return;
+    float* sc = scales + st * 3 * kStep + lane;
+    const float f = x.v == 0.f ? 5.9604645e-8f : x.v;   // a zero scale (codes all 0) counts in the row sum alone
+    sc[0] = x.k * a.scale_log2;
+    sc[kStep] = log2f(f);
+    sc[2 * kStep] = 1.0f / f;
+  };
+  // copies of step i into stage st
+  auto issue = [&](int i, int st, int32_t page, Scales& sc) {
     if (i < steps) {
       const int key = first + i * (kWarps * kStep), s = key & page_mask;
       const bool ok = page_ok(page, a.pool.num_pages);
@@ -264,8 +289,8 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
       const int valid = ok ? min(k1 - key, kStep) : 0;
       if (INT8) {
         const int64_t so = page * a.pool.sstride_page + (s + lane) * a.pool.sstride_t + kvh * a.pool.sstride_h;
-        pend_k = lane < valid ? __half2float(a.pool.ks[so]) : 0.f;
-        pend_v = lane < valid ? __half2float(a.pool.vs[so]) : 0.f;
+        sc.k = lane < valid ? __half2float(a.pool.ks[so]) : 0.f;
+        sc.v = lane < valid ? __half2float(a.pool.vs[so]) : 0.f;
       }
       const uint32_t dst = ring_s + st * 2 * S::BYTES;
       if (maps.ok && valid == kStep) {
@@ -297,10 +322,10 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
     }
     cp_commit();
   };
-  int32_t page = entry_at(0), page1 = entry_at(1);
-  issue(0, 0, page);
-  page = entry_at(2);
-  issue(1, 1, page1);
+  Scales sc_a{}, sc_b{};
+  issue(0, 0, page, sc_a);
+  issue(1, 1, page1, sc_b);
+  page = page2;
 
   // ---- this lane's rows r8 and r8 + 8: limits and Q fragments, while the first copies are under way
   int lim[2];
@@ -335,6 +360,8 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
   for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
+  if (steps > 0) keep_scales(0, sc_a);
+  if (steps > 1) keep_scales(1, sc_b);
   int st = 0;
   uint32_t laps = 0;        // bit s: parity of stage s's next TMA fill
   for (int i = 0; i < steps; ++i) {
@@ -344,7 +371,8 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
       laps ^= 1u << st;
     }
     __syncwarp();
-    issue(i + 2, st == 0 ? kStages - 1 : st - 1, page);      // into the stage that step i - 1 used
+    const int freed = st == 0 ? kStages - 1 : st - 1;        // the stage that step i - 1 used
+    issue(i + 2, freed, page, sc_a);
     page = entry_at(i + 3);
     const uint32_t ks_s = ring_s + st * 2 * S::BYTES;
     const uint32_t vs_s = ks_s + S::BYTES;
@@ -493,6 +521,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
         }
       }
     }
+    if (i + 2 < steps) keep_scales(freed, sc_a);      // the loads have had this step's time
   }
   cp_wait<0>();
 #pragma unroll
@@ -596,7 +625,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 // Results of one row (token t, query head h): prefix results lie in slots 0 ..
 // pre - 1, the pieces of the line that the row block's key tiles lie in.
 __device__ __forceinline__ int prefix_results(const SharedPlan& p, int t, int h) {
-  if (!p.pre_tile) return p.pre_splits;
+  if (!p.pre_tile || p.pre_pieces > 0) return p.pre_splits;
   const int kvh = h / p.group;
   const int packed = t * p.group + h - kvh * p.group;
   const int first = (kvh * p.pre_rows + packed / 256) * p.pre_tiles;
@@ -681,11 +710,11 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const __grid_constant__ 
 
 // Joins a row's results: W warps per (token, query head).  Every warp weighs
 // all slots (one or two per lane); warp w adds the O rows of slots w, w + W, ..,
-// four loads in flight, and the warps' sums meet in shared memory.  Moves
+// eight loads in flight, and the warps' sums meet in shared memory.  Moves
 // count * d * 4 bytes a row, mostly out of L2; with few rows it is bound by
-// latency, which is what W is for.
+// latency: W is as large as leaves one wave of blocks.
 template <int D, int W>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ SharedArgs a) {
+__global__ void __launch_bounds__(256, 4) join_kernel(const __grid_constant__ SharedArgs a) {
   constexpr int V = D / 32;
   __shared__ float sums[8][D];
   const int Hq = a.pool.H * a.plan.group;
@@ -722,10 +751,11 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Share
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   float acc[V] = {};
-  for (int i0 = part; i0 < count; i0 += 4 * W) {
-    float w[4], f[4][V];
+  constexpr int U = 8;
+  for (int i0 = part; i0 < count; i0 += U * W) {
+    float w[U], f[U][V];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < U; ++k) {
       const int i = i0 + k * W;
       w[k] = __shfl_sync(0xffffffffu, i < 32 ? wgt[0] : wgt[1], i & 31);
       if (i >= count) w[k] = 0.f;
@@ -747,7 +777,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Share
       }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < U; ++k) {
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] += w[k] * f[k][v];
     }
@@ -807,8 +837,10 @@ tm_status launch(const SharedArgs& a, int d, bool int8, DevErr err, cudaStream_t
   const int64_t rows = a.T * a.pool.H * p.group;
   if (rows >= 8192 || p.slots <= 2)
     return launch_kernel(d == 128 ? join_rows_kernel<128> : join_rows_kernel<64>, ceil_div(rows, 32), 256, 0, after, stream, a);
-  const int W = rows >= 1024 ? 4 : 8;
-  auto join = d == 128 ? (W == 4 ? join_kernel<128, 4> : join_kernel<128, 8>) : (W == 4 ? join_kernel<64, 4> : join_kernel<64, 8>);
+  constexpr int64_t kResident = 4 * kSmsB200;       // blocks of 256 threads at 64 registers
+  const int W = rows <= kResident ? 8 : (rows <= 2 * kResident ? 4 : (rows <= 4 * kResident ? 2 : 1));
+  auto join = d == 128 ? (W == 8 ? join_kernel<128, 8> : W == 4 ? join_kernel<128, 4> : W == 2 ? join_kernel<128, 2> : join_kernel<128, 1>)
+                       : (W == 8 ? join_kernel<64, 8> : W == 4 ? join_kernel<64, 4> : W == 2 ? join_kernel<64, 2> : join_kernel<64, 1>);
   return launch_kernel(join, ceil_div(rows, 8 / W), 256, 0, after, stream, a);
 }
 

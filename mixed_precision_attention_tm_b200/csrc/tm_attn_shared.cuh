@@ -31,6 +31,8 @@ constexpr float kPOffset = 6.0f;
 // the own tokens or the prefix; more rows go to the tile kernel.
 constexpr int kSplitRowsOwn = 64, kSplitRowsPrefix = 16;
 constexpr int kMostSplits = 30;
+// Key tiles that a row block's start and end cost a CTA of the tile kernel (about 6 us at 1.9 us a tile).
+constexpr int kSplitBlockTiles = 3;
 
 struct SharedPlan {
   int group;                  // query heads per K/V head
@@ -40,6 +42,7 @@ struct SharedPlan {
   int own_chunk;              // keys per split
   int pre_chunk;              // the same; on the tile kernel: key tiles per CTA
   int pre_tiles, pre_ctas;    // tile kernel: key tiles of the prefix, CTAs
+  int pre_pieces;             // tile kernel: pieces of a row block, 0: pieces of the whole line
   int slots;                  // own_splits + pre_splits
   int64_t ml_bytes, bytes;    // workspace: (m, l) of every slot and row, then O
 };

@@ -67,7 +67,7 @@ struct CfgT {
   static constexpr int LOADED = INT8 ? CODES : SLOT;   // bytes that a tile's copies bring
   // Registers at launch, and after the split over softmax, control and (INT8) two conversion warpgroups.
   static constexpr int THREADS = INT8 ? 640 : 384, LAUNCH_REGS = INT8 ? 96 : 168;
-  static constexpr int SOFTMAX_REGS = INT8 ? 168 : 216, CONTROL_REGS = INT8 ? 64 : 72, CONVERT_REGS = INT8 ? 40 : 0;
+  static constexpr int SOFTMAX_REGS = INT8 ? 152 : 216, CONTROL_REGS = INT8 ? 64 : 72, CONVERT_REGS = INT8 ? 56 : 0;
   static_assert(2 * 128 * SOFTMAX_REGS + 128 * CONTROL_REGS + 256 * CONVERT_REGS == THREADS * LAUNCH_REGS,
                 "register split");
   static_assert(SMEM <= 232448, "shared memory per CTA");
@@ -160,9 +160,15 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
   // ---- this CTA's segments, walked by every role alike
   int unit = 0, unit_end = 1;         // prefix: key tiles of the line
   if (prefix) {
-    unit = blockIdx.x * p.pre_chunk;
-    const int line = H * p.pre_rows * p.pre_tiles;
-    unit_end = p.pre_chunk < line - unit ? unit + p.pre_chunk : line;
+    if (p.pre_pieces > 0) {
+      const int rb = static_cast<int>(blockIdx.x) / p.pre_pieces, piece = static_cast<int>(blockIdx.x) - rb * p.pre_pieces;
+      unit = rb * p.pre_tiles + piece * p.pre_chunk;
+      unit_end = min(unit + p.pre_chunk, (rb + 1) * p.pre_tiles);
+    } else {
+      const int line = H * p.pre_rows * p.pre_tiles;
+      unit = blockIdx.x * p.pre_chunk;
+      unit_end = p.pre_chunk < line - unit ? unit + p.pre_chunk : line;
+    }
   }
   auto next_segment = [&](int& u, Segment& s) -> bool {
     if (u >= unit_end) return false;
@@ -171,7 +177,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       const int rb = u / p.pre_tiles;
       const int first = u - rb * p.pre_tiles;
       const int count = min(p.pre_tiles - first, unit_end - u);
-      s.slot = static_cast<int>(blockIdx.x) - (u - first) / p.pre_chunk;
+      s.slot = p.pre_pieces > 0 ? first / p.pre_chunk : static_cast<int>(blockIdx.x) - (u - first) / p.pre_chunk;
       u += count;
       s.kvh = rb / p.pre_rows;
       s.row0 = (rb - s.kvh * p.pre_rows) * 256;
@@ -219,35 +225,6 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
     return true;
   };
 
-  // ---- setup
-  if (threadIdx.x == 0) {
-    mbar_init(bar(T_QFULL), 1);
-    mbar_init(bar(T_QEMPTY), 2);
-    for (int i = 0; i < 4; ++i) mbar_init(bar(T_SFULL + i), 1);
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(T_ODONE + t), 1);
-      mbar_init(bar(T_DRAIN + t), 1);
-      mbar_init(bar(T_OLAST + t), 1);
-    }
-    for (int s = 0; s < C::NSLOT; ++s) {
-      mbar_init(bar(T_FULL + s), INT8 ? 4 : 1);
-      mbar_init(bar(T_EMPTY + s), 2);
-      if (INT8) mbar_init(bar(T_CODES + s), 1);
-    }
-    *abort_flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == 9) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
-    tc_fence_before();
-  }
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  int u = unit;
-  Segment sg;
-
   // Page of key `key` of a segment: -1 behind its end, -2 where it cannot be used
   const int shift = a.pool.page_shift;
   const int page_mask = (1 << shift) - 1;
@@ -261,6 +238,172 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
     const int32_t page = entry_at(s, key);
     return page_ok(page, a.pool.num_pages) ? page : -2;
   };
+
+  // ---- setup.  The loader makes its own barriers and begins at once; the others wait for them and for tensor
+  // memory at the first __syncthreads, which it joins after its first copies.
+  int u = unit;
+  Segment sg;
+  if (warp == 8) {
+    if (lane == 0) {
+      prefetch_tmap(&maps.q);
+      prefetch_tmap(&maps.kv.k);
+      prefetch_tmap(&maps.kv.v);
+      mbar_init(bar(T_QFULL), 1);
+      mbar_init(bar(T_QEMPTY), 2);
+      for (int i = 0; i < 4; ++i) mbar_init(bar(T_SFULL + i), 1);
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(bar(T_ODONE + t), 1);
+        mbar_init(bar(T_DRAIN + t), 1);
+        mbar_init(bar(T_OLAST + t), 1);
+      }
+      for (int s = 0; s < C::NSLOT; ++s) {
+        mbar_init(bar(T_FULL + s), INT8 ? 4 : 1);
+        mbar_init(bar(T_EMPTY + s), 2);
+        if (INT8) mbar_init(bar(T_CODES + s), 1);
+      }
+      *abort_flag = 0;
+      fence_barrier_init();
+    }
+    __syncwarp();
+    regs_dec<C::CONTROL_REGS>();
+    // ======================= loader =======================
+    uint32_t n = 0, qn = 0;
+    const int box_shift = shift < 7 ? shift : 7;       // key rows of a copy
+    const int boxes = 128 >> box_shift;
+    const int LANDED = INT8 ? T_CODES : T_FULL;
+    constexpr uint32_t DST = INT8 ? C::SLOT / 2 : 0;
+    // a whole tile: lane i copies box i, whose page it holds
+    auto copy_boxes = [&](const CUtensorMap* map, uint32_t slot, int32_t page, int key) {
+      const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT + DST;
+      if (lane == 0) mbar_arrive_expect_tx(bar(LANDED + slot), C::LOADED);
+      __syncwarp();
+      if (lane < boxes) {
+        const int32_t s0 = key & page_mask;
+        const int32_t c1 = maps.kv.heads_inner ? sg.kvh : s0, c2 = maps.kv.heads_inner ? s0 : sg.kvh;
+#pragma unroll
+        for (int hh = 0; hh < (INT8 ? 1 : D / 64); ++hh)
+          tma_load_4d(tile + hh * C::HALF + (lane << box_shift) * (INT8 ? D : 128), map, bar(LANDED + slot), hh * 64,
+                      c1, c2, page);
+      }
+      __syncwarp();
+    };
+    // a ragged tile: row by row; the page of each run of 16 keys is in lane `run`
+    auto copy_rows = [&](const uint8_t* base, uint32_t slot, int32_t page, int key0) {
+      constexpr int ROW = D * (INT8 ? 1 : 2), PIECES = ROW / 16, RPI = 32 / PIECES;
+      const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT + DST;
+      const int c = lane % PIECES;
+#pragma unroll 1
+      for (int run = 0; run < 8; ++run) {
+        const int32_t pg = __shfl_sync(0xffffffffu, page, run);
+        const int key = key0 + 16 * run;
+        const uint8_t* src = base + c * 16 + (pg >= 0 ? pg * a.pool.stride_page + (key & page_mask) * a.pool.stride_t : 0);
+#pragma unroll
+        for (int i = 0; i < 16 / RPI; ++i) {
+          const int rr = i * RPI + lane / PIECES;
+          const int r = 16 * run + rr;
+          const uint32_t dst = INT8 && D == 64 ? tile + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)
+                                               : tile + (c >> 3) * C::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          const bool real = pg >= 0 && key + rr < sg.lk;
+          cp16(dst, real ? src + rr * a.pool.stride_t : base, real);
+        }
+      }
+      cp_commit();
+    };
+    auto acquire = [&](uint32_t i) {
+      if (i >= C::NSLOT) mbar_wait_warp(bar(T_EMPTY + i % C::NSLOT), (i / C::NSLOT - 1) & 1, err, abort_flag);
+    };
+    auto landed = [&](uint32_t b) {
+      fence_async_shared();      // read by tcgen05.mma
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b);
+    };
+    bool met = false;          // the setup's __syncthreads
+    auto meet = [&]() {
+      if (!met) __syncthreads();
+      met = true;
+    };
+    while (next_segment(u, sg)) {
+      const int nj = sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
+      if (nj == 0) continue;
+      // pages of key tile j: box i's in lane i
+      const int step = 128 / boxes;
+      auto my_page = [&](int j) -> int32_t {
+        const int key = sg.key0 + j * 128 + lane * step;
+        return j < nj && lane < boxes ? page_at(sg, key) : -1;
+      };
+      int32_t page = my_page(0);
+      // Q of both tiles, once the MMAs of the last segment have read theirs
+      if (qn > 0) mbar_wait_warp(bar(T_QEMPTY), (qn - 1) & 1, err, abort_flag);
+      ++qn;
+      const uint32_t gg = static_cast<uint32_t>(g);
+      if (maps.q_tma) {
+        if (lane == 0) mbar_arrive_expect_tx(bar(T_QFULL), 2 * C::Q_BYTES);
+        __syncwarp();
+        if (lane < 2 * (D / 64)) {
+          const int t = lane & 1, hh = lane >> 1;
+          const int32_t token = sg.start + (sg.row0 + 128 * t) / g;
+          tma_load_3d(sbase + t * C::Q_BYTES + hh * C::HALF, &maps.q, bar(T_QFULL), hh * 64, sg.kvh * g, token);
+        }
+        __syncwarp();
+      } else {
+        constexpr int QP = D / 8;
+        const int qc = lane % QP;
+        const uint32_t row0 = static_cast<uint32_t>(sg.row0);
+        const __half* qbase = a.q + static_cast<int64_t>(sg.start) * a.q_t + static_cast<int64_t>(sg.kvh) * g * a.q_h + qc * 8;
+#pragma unroll 2
+        for (int i = 0; i < 8 * QP; ++i) {
+          const int pr = i * (32 / QP) + lane / QP;
+          const bool real = pr < sg.rows;
+          const uint32_t row = row0 + pr, tok = row / gg;
+          const __half* src = real ? qbase + tok * a.q_t + (row - tok * gg) * a.q_h : a.q;
+          const int r = pr & 127;
+          cp16(sbase + (pr >> 7) * C::Q_BYTES + (qc >> 3) * C::HALF + r * 128 + (((qc & 7) ^ (r & 7)) << 4), src, real);
+        }
+        cp_commit();
+        cp_wait<0>();
+        landed(bar(T_QFULL));
+      }
+      for (int j = 0; j < nj; ++j, ++n) {
+        const int key0 = sg.key0 + j * 128;
+        const int32_t next = my_page(j + 1);
+        if (page == -2) dev_error(err, TM_DEVERR_SEQLEN);
+        const uint32_t i = 2 * n;
+        if (maps.kv.ok && key0 + 128 <= sg.lk && __all_sync(0xffffffffu, lane >= boxes || page >= 0)) {
+          const int key = key0 + lane * step;
+          acquire(i);
+          copy_boxes(&maps.kv.k, i % C::NSLOT, page, key);
+          acquire(i + 1);
+          copy_boxes(&maps.kv.v, (i + 1) % C::NSLOT, page, key);
+        } else {
+          const int32_t run_page = __shfl_sync(0xffffffffu, page, ((lane & 7) * 16) >> box_shift);
+          acquire(i);
+          copy_rows(a.pool.k + sg.kvh * a.pool.stride_h, i % C::NSLOT, run_page, key0);
+          acquire(i + 1);
+          copy_rows(a.pool.v + sg.kvh * a.pool.stride_h, (i + 1) % C::NSLOT, run_page, key0);
+          cp_wait<1>();
+          landed(bar(LANDED + i % C::NSLOT));
+          cp_wait<0>();
+          landed(bar(LANDED + (i + 1) % C::NSLOT));
+        }
+        page = next;
+        meet();
+      }
+    }
+    meet();
+    // every copy has landed before the block may end
+    volatile int never = 0;
+    if (qn > 0) mbar_wait_warp(bar(T_QFULL), (qn - 1) & 1, err, &never);
+    for (uint32_t i = 2 * n > C::NSLOT ? 2 * n - C::NSLOT : 0; i < 2 * n; ++i)
+      mbar_wait_warp(bar(LANDED + i % C::NSLOT), (i / C::NSLOT) & 1, err, &never);
+  } else {
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
 
   if (INT8 && warp >= 12) {
     // ======================= conversion of codes (warpgroup v: K or V; thread r: key row r of each tile) ====
@@ -332,130 +475,6 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
     }
   } else if (warp >= 8) {
     regs_dec<C::CONTROL_REGS>();
-    if (warp == 8) {
-      // ======================= loader =======================
-      uint32_t n = 0, qn = 0;
-      const int box_shift = shift < 7 ? shift : 7;       // key rows of a copy
-      const int boxes = 128 >> box_shift;
-      const int LANDED = INT8 ? T_CODES : T_FULL;
-      constexpr uint32_t DST = INT8 ? C::SLOT / 2 : 0;
-      // a whole tile: lane i copies box i, whose page it holds
-      auto copy_boxes = [&](const CUtensorMap* map, uint32_t slot, int32_t page, int key) {
-        const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT + DST;
-        if (lane == 0) mbar_arrive_expect_tx(bar(LANDED + slot), C::LOADED);
-        __syncwarp();
-        if (lane < boxes) {
-          const int32_t s0 = key & page_mask;
-          const int32_t c1 = maps.kv.heads_inner ? sg.kvh : s0, c2 = maps.kv.heads_inner ? s0 : sg.kvh;
-#pragma unroll
-          for (int hh = 0; hh < (INT8 ? 1 : D / 64); ++hh)
-            tma_load_4d(tile + hh * C::HALF + (lane << box_shift) * (INT8 ? D : 128), map, bar(LANDED + slot), hh * 64,
-                        c1, c2, page);
-        }
-        __syncwarp();
-      };
-      // a ragged tile: row by row; the page of each run of 16 keys is in lane `run`
-      auto copy_rows = [&](const uint8_t* base, uint32_t slot, int32_t page, int key0) {
-        constexpr int ROW = D * (INT8 ? 1 : 2), PIECES = ROW / 16, RPI = 32 / PIECES;
-        const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT + DST;
-        const int c = lane % PIECES;
-#pragma unroll 1
-        for (int run = 0; run < 8; ++run) {
-          const int32_t pg = __shfl_sync(0xffffffffu, page, run);
-          const int key = key0 + 16 * run;
-          const uint8_t* src = base + c * 16 + (pg >= 0 ? pg * a.pool.stride_page + (key & page_mask) * a.pool.stride_t : 0);
-#pragma unroll
-          for (int i = 0; i < 16 / RPI; ++i) {
-            const int rr = i * RPI + lane / PIECES;
-            const int r = 16 * run + rr;
-            const uint32_t dst = INT8 && D == 64 ? tile + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)
-                                                 : tile + (c >> 3) * C::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-            const bool real = pg >= 0 && key + rr < sg.lk;
-            cp16(dst, real ? src + rr * a.pool.stride_t : base, real);
-          }
-        }
-        cp_commit();
-      };
-      auto acquire = [&](uint32_t i) {
-        if (i >= C::NSLOT) mbar_wait_warp(bar(T_EMPTY + i % C::NSLOT), (i / C::NSLOT - 1) & 1, err, abort_flag);
-      };
-      auto landed = [&](uint32_t b) {
-        fence_async_shared();      // read by tcgen05.mma
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b);
-      };
-      while (next_segment(u, sg)) {
-        const int nj = sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
-        if (nj == 0) continue;
-        // Q of both tiles, once the MMAs of the last segment have read theirs
-        if (qn > 0) mbar_wait_warp(bar(T_QEMPTY), (qn - 1) & 1, err, abort_flag);
-        ++qn;
-        const uint32_t gg = static_cast<uint32_t>(g);
-        if (maps.q_tma) {
-          if (lane == 0) mbar_arrive_expect_tx(bar(T_QFULL), 2 * C::Q_BYTES);
-          __syncwarp();
-          if (lane < 2 * (D / 64)) {
-            const int t = lane & 1, hh = lane >> 1;
-            const int32_t token = sg.start + (sg.row0 + 128 * t) / g;
-            tma_load_3d(sbase + t * C::Q_BYTES + hh * C::HALF, &maps.q, bar(T_QFULL), hh * 64, sg.kvh * g, token);
-          }
-          __syncwarp();
-        } else {
-          constexpr int QP = D / 8;
-          const int qc = lane % QP;
-          const uint32_t row0 = static_cast<uint32_t>(sg.row0);
-          const __half* qbase = a.q + static_cast<int64_t>(sg.start) * a.q_t + static_cast<int64_t>(sg.kvh) * g * a.q_h + qc * 8;
-#pragma unroll 4
-          for (int i = 0; i < 8 * QP; ++i) {
-            const int pr = i * (32 / QP) + lane / QP;
-            const bool real = pr < sg.rows;
-            const uint32_t row = row0 + pr, tok = row / gg;
-            const __half* src = real ? qbase + tok * a.q_t + (row - tok * gg) * a.q_h : a.q;
-            const int r = pr & 127;
-            cp16(sbase + (pr >> 7) * C::Q_BYTES + (qc >> 3) * C::HALF + r * 128 + (((qc & 7) ^ (r & 7)) << 4), src, real);
-          }
-          cp_commit();
-          cp_wait<0>();
-          landed(bar(T_QFULL));
-        }
-        // lanes 0-7: pages of the 16-key runs (box i's page is in lane i of page_of_box)
-        const int step = 128 / boxes;
-        auto my_page = [&](int j) -> int32_t {
-          const int key = sg.key0 + j * 128 + lane * step;
-          return j < nj && lane < boxes ? page_at(sg, key) : -1;
-        };
-        int32_t page = my_page(0);
-        for (int j = 0; j < nj; ++j, ++n) {
-          const int key0 = sg.key0 + j * 128;
-          const int32_t next = my_page(j + 1);
-          if (page == -2) dev_error(err, TM_DEVERR_SEQLEN);
-          const uint32_t i = 2 * n;
-          if (maps.kv.ok && key0 + 128 <= sg.lk && __all_sync(0xffffffffu, lane >= boxes || page >= 0)) {
-            const int key = key0 + lane * step;
-            acquire(i);
-            copy_boxes(&maps.kv.k, i % C::NSLOT, page, key);
-            acquire(i + 1);
-            copy_boxes(&maps.kv.v, (i + 1) % C::NSLOT, page, key);
-          } else {
-            const int32_t run_page = __shfl_sync(0xffffffffu, page, ((lane & 7) * 16) >> box_shift);
-            acquire(i);
-            copy_rows(a.pool.k + sg.kvh * a.pool.stride_h, i % C::NSLOT, run_page, key0);
-            acquire(i + 1);
-            copy_rows(a.pool.v + sg.kvh * a.pool.stride_h, (i + 1) % C::NSLOT, run_page, key0);
-            cp_wait<1>();
-            landed(bar(LANDED + i % C::NSLOT));
-            cp_wait<0>();
-            landed(bar(LANDED + (i + 1) % C::NSLOT));
-          }
-          page = next;
-        }
-      }
-      // every copy has landed before the block may end
-      volatile int never = 0;
-      if (qn > 0) mbar_wait_warp(bar(T_QFULL), (qn - 1) & 1, err, &never);
-      for (uint32_t i = 2 * n > C::NSLOT ? 2 * n - C::NSLOT : 0; i < 2 * n; ++i)
-        mbar_wait_warp(bar(LANDED + i % C::NSLOT), (i / C::NSLOT) & 1, err, &never);
-    }
     if (warp == 9 || warp == 10) {
       // ======================= tcgen05 issuers (warp 9: tile A, warp 10: tile B) ====
       // They never touch shared memory: the wait helper polls for them.
@@ -753,11 +772,12 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       }
     }
   }
+  }
 
   __syncthreads();
   if (warp == 9) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(*tmem_slot, 512);
   }
   pdl_wait();      // whoever waits for this kernel has waited for the one before it
 }
