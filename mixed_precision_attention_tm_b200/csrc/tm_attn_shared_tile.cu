@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
   // ---- setup.  The loader makes its own barriers and begins at once; the others wait for them and for tensor
   // memory at the first __syncthreads, which it joins after its first copies.
   int u = unit;
-  Segment sg;
+  Segment sg{};
   if (warp == 8) {
     if (lane == 0) {
       prefetch_tmap(&maps.q);

@@ -71,20 +71,55 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 
 enum { kNoCache = 0, kCacheF16 = 1, kCacheI8 = 2 };
 
-// A warp takes one token and every `parts`-th group of 32 / (D / 8) heads; a
-// lane holds 8 consecutive values of a head (one 16-byte load).  U groups are
-// loaded before the first is used, to keep several loads in flight.
-template <int D, int CACHE>
+// A warp takes one token and every `parts`-th item: 512 / D heads of Q, K or V.
+// A lane holds 16 values of a head, in two 16-byte pieces chosen so that both
+// members of every pair are its own: pieces l and l + rot / 16 in the half
+// layout (and the unrotated rest two by two), neighbours in the interleaved
+// one.  So the rotation needs no shuffles; the norm's sum takes log2(D / 16).
+// U items are loaded before the first is used, to keep loads in flight.
+template <int D, int CACHE, bool NORM>
 __global__ void __launch_bounds__(kTokenWarps * 32) token_kernel(const __grid_constant__ TokenArgs a, DevErr err) {
-  constexpr int LPR = D / 8;          // lanes of a row
-  constexpr int RPW = 32 / LPR;       // rows of a warp
-  constexpr int U = 4;
+  constexpr int LPR = D / 16;         // lanes of a head
+  constexpr int RPW = 32 / LPR;       // heads of an item
+  constexpr int U = 2;
   __shared__ __align__(16) float2 trig[kTokenWarps][64];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t job = static_cast<int64_t>(blockIdx.x) * kTokenWarps + warp;
-  const int64_t t = job / a.parts;
-  const int part = static_cast<int>(job - t * a.parts);
+  int64_t t = job;
+  int part = 0;
+  if (a.parts > 1) {                  // then a.T * a.parts stays below 2^31
+    t = static_cast<uint32_t>(job) / static_cast<uint32_t>(a.parts);
+    part = static_cast<int>(job - t * a.parts);
+  }
   if (t >= a.T) return;
+
+  // this lane's head of an item, and its two pieces
+  const int l = lane & (LPR - 1), sub = lane / LPR;
+  const int pairs = a.rot >> 4;       // lanes of a head that rotate
+  const bool turned = a.rope && l < pairs;
+  int pa = 2 * l, pb = 2 * l + 1;     // unrotated: rot / 8 + 2 (l - rot / 16) = 2 l
+  if (turned && !a.interleaved) {
+    pa = l;
+    pb = l + pairs;
+  }
+
+  const int iq = (a.hq + RPW - 1) / RPW, ik = (a.hk + RPW - 1) / RPW, iv = (a.hv + RPW - 1) / RPW;
+  const int items = iq + ik + iv;
+  uint4 raw[U][2];
+  auto load = [&](int it, uint4 (&x)[2]) {
+    const bool isq = it < iq, isk = it < iq + ik;        // the same for the whole warp
+    const Rows& r = isq ? a.q : (isk ? a.k : a.v);
+    const int h = (it - (isq ? 0 : (isk ? iq : iq + ik))) * RPW + sub;
+    x[0] = x[1] = make_uint4(0, 0, 0, 0);
+    if (it < items && h < (isq ? a.hq : (isk ? a.hk : a.hv))) {
+      const uint4* src = reinterpret_cast<const uint4*>(r.in + t * r.in_t + h * r.in_h);      // in place: not ld.nc
+      x[0] = src[pa];
+      x[1] = src[pb];
+    }
+  };
+  // before the token's sequence, place and page are looked up, a chain of loads of its own
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(part + u * a.parts, raw[u]);
 
   int64_t pos;
   int64_t slot_row = -1, slot_scale = 0;   // where the token's K and V go (CACHE)
@@ -118,155 +153,131 @@ __global__ void __launch_bounds__(kTokenWarps * 32) token_kernel(const __grid_co
     }
   }
 
-  const int half_rot = a.rot >> 1;
+  // sines and cosines of the token, up to two pairs per lane, while the loads are under way
+  float cs[8], sn[8];
   if (a.rope) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int i = lane + 32 * r;
-      if (i < half_rot) {
+      if (i < (a.rot >> 1)) {
         const uint64_t turn = static_cast<uint64_t>(pos) * a.turns[i];
         const int32_t top = static_cast<int32_t>(static_cast<uint32_t>(turn >> 32));
-        float sn, cs;
-        sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &sn, &cs);   // 2^-31: half turns
-        trig[warp][i] = make_float2(cs * a.mscale, sn * a.mscale);
+        float s, c;
+        sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
+        trig[warp][i] = make_float2(c * a.mscale, s * a.mscale);
       }
     }
     __syncwarp();
-  }
-
-  // this lane's place in a row and its eight (cos, sin): in the half layout
-  // its values are the first or second members of pairs i0 .. i0 + 7, and the
-  // partner values sit `half_rot` away, half_rot / 8 lanes off; in the
-  // interleaved one it holds the whole pairs i0 .. i0 + 3.
-  const int l = lane & (LPR - 1);
-  const int sub = lane / LPR;
-  const int rot_lanes = a.rot >> 3, half_lanes = a.rot >> 4;
-  const bool turned = a.rope && l < rot_lanes;
-  const bool second = !a.interleaved && l >= half_lanes;
-  const int partner = a.interleaved ? lane : (turned ? (second ? lane - half_lanes : lane + half_lanes) : lane);
-  float cs[8], sn[8];
-  if (turned) {
-    if (a.interleaved) {
+    if (turned) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = trig[warp][4 * l + e];
+      for (int e = 0; e < 8; e += 2) {
+        const float4 f = *reinterpret_cast<const float4*>(&trig[warp][8 * l + e]);
         cs[e] = f.x;
         sn[e] = f.y;
-      }
-    } else {
-      const int i0 = 8 * (second ? l - half_lanes : l);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 f = trig[warp][i0 + e];
-        cs[e] = f.x;
-        sn[e] = second ? f.y : -f.y;
+        cs[e + 1] = f.z;
+        sn[e + 1] = f.w;
       }
     }
   }
 
-  const int heads = a.hq + a.hk + a.hv;
-  const int groups = (heads + RPW - 1) / RPW;
-  for (int g0 = part; g0 < groups; g0 += a.parts * U) {
-    uint4 raw[U];
+  for (int it0 = part; it0 < items; it0 += a.parts * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = (g0 + u * a.parts) * RPW + sub;
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (h < heads) {
-        const bool isq = h < a.hq, isk = h < a.hq + a.hk;
-        const Rows& r = isq ? a.q : (isk ? a.k : a.v);
-        const int hh = isq ? h : (isk ? h - a.hq : h - a.hq - a.hk);
-        raw[u] = *(reinterpret_cast<const uint4*>(r.in + t * r.in_t + hh * r.in_h) + l);   // in place: not ld.nc
+      const int it = it0 + u * a.parts;
+      if (it >= items) break;                            // the same for the whole warp
+      const bool isq = it < iq, isk = !isq && it < iq + ik, isv = !isq && !isk;
+      const int h = (it - (isq ? 0 : (isk ? iq : iq + ik))) * RPW + sub;
+      const bool real = h < (isq ? a.hq : (isk ? a.hk : a.hv));
+      float x[2][8];
+      unpack8(raw[u][0], x[0]);
+      unpack8(raw[u][1], x[1]);
+      load(it + a.parts * U, raw[u]);                    // the item after the next ones, into the registers just freed
+      if (NORM && !isv) {
+        const __half* w = isq ? a.q.weight : a.k.weight;
+        if (w != nullptr) {
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss += x[0][e] * x[0][e] + x[1][e] * x[1][e];
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+          float wf[8];
+          unpack8(__ldg(reinterpret_cast<const uint4*>(w) + pa), wf);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[0][e] = x[0][e] * inv * wf[e];
+          unpack8(__ldg(reinterpret_cast<const uint4*>(w) + pb), wf);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[1][e] = x[1][e] * inv * wf[e];
+        }
       }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int g = g0 + u * a.parts;
-      if (g >= groups) break;              // the same for the whole warp
-      const int h = g * RPW + sub;
-      const bool isq = h < a.hq, isk = !isq && h < a.hq + a.hk;
-      const bool isv = !isq && !isk;
-      const int hh = isq ? h : (isk ? h - a.hq : h - a.hq - a.hk);
-      const __half* w = isq ? a.q.weight : (isk ? a.k.weight : nullptr);
-      float x[8];
-      unpack8(raw[u], x);
-      // the norm's sum runs over the row's lanes; all lanes take part in the
-      // shuffles whatever their row
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (w != nullptr) {
-        const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-        float wf[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(w) + l), wf);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * wf[e];
-      }
-      if (a.rope) {
+      if (turned && !isv) {
         if (a.interleaved) {
-          if (turned && !isv) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float p = x[2 * e], q = x[2 * e + 1];
-              x[2 * e] = p * cs[e] - q * sn[e];
-              x[2 * e + 1] = p * sn[e] + q * cs[e];
-            }
+          for (int e = 0; e < 8; ++e) {
+            float& p = x[e >> 2][2 * (e & 3)];
+            float& q = x[e >> 2][2 * (e & 3) + 1];
+            const float y = p * cs[e] - q * sn[e];
+            q = p * sn[e] + q * cs[e];
+            p = y;
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float y = __shfl_sync(0xffffffffu, x[e], partner);
-            if (turned && !isv) x[e] = x[e] * cs[e] + y * sn[e];
+            const float y = x[0][e] * cs[e] - x[1][e] * sn[e];
+            x[1][e] = x[0][e] * sn[e] + x[1][e] * cs[e];
+            x[0][e] = y;
           }
         }
       }
-      if (CACHE == kCacheI8) {
+      if (CACHE == kCacheI8 && !isq) {
         // absmax as integer bits: a NaN compares above everything and so
         // reaches the scale
         uint32_t m = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+        for (int e = 0; e < 8; ++e)
+          m = max(m, max(__float_as_uint(x[0][e]) & 0x7fffffffu, __float_as_uint(x[1][e]) & 0x7fffffffu));
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (!isq && h < heads && slot_row >= 0) {
+        if (real && slot_row >= 0) {
           const __half s16 = __float2half_rn(__fdiv_rn(__uint_as_float(m), 127.0f));
           const float s = __half2float(s16);
-          uint32_t c[2] = {0, 0};
+          uint32_t c[2][2] = {{0, 0}, {0, 0}};
           if (s != 0.f) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              int v = __float2int_rn(__fdiv_rn(x[e], s));
+            for (int e = 0; e < 16; ++e) {
+              int v = __float2int_rn(__fdiv_rn(x[e >> 3][e & 7], s));
               v = max(-127, min(127, v));
-              c[e >> 2] |= static_cast<uint32_t>(v & 255) << (8 * (e & 3));
+              c[e >> 3][(e >> 2) & 1] |= static_cast<uint32_t>(v & 255) << (8 * (e & 3));
             }
           }
-          uint8_t* base = isk ? a.pool.k : a.pool.v;
-          *reinterpret_cast<uint2*>(base + slot_row + hh * a.pool.stride_h + 8 * l) = make_uint2(c[0], c[1]);
-          if (l == 0) (isk ? a.pool.ks : a.pool.vs)[slot_scale + hh * a.pool.sstride_h] = s16;
+          uint8_t* row = (isk ? a.pool.k : a.pool.v) + slot_row + h * a.pool.stride_h;
+          *reinterpret_cast<uint2*>(row + 8 * pa) = make_uint2(c[0][0], c[0][1]);
+          *reinterpret_cast<uint2*>(row + 8 * pb) = make_uint2(c[1][0], c[1][1]);
+          if (l == 0) (isk ? a.pool.ks : a.pool.vs)[slot_scale + h * a.pool.sstride_h] = s16;
         }
+        continue;
       }
-      if (h >= heads) continue;
+      if (!real) continue;
+      uint4* dst;
       if (CACHE == kNoCache || isq) {
         const Rows& r = isq ? a.q : a.k;
-        *(reinterpret_cast<uint4*>(r.out + t * r.out_t + hh * r.out_h) + l) = pack8(x);
-      } else if (CACHE == kCacheF16 && slot_row >= 0) {
-        uint8_t* base = isk ? a.pool.k : a.pool.v;
-        *reinterpret_cast<uint4*>(base + slot_row + hh * a.pool.stride_h + 16 * l) = pack8(x);
+        dst = reinterpret_cast<uint4*>(r.out + t * r.out_t + h * r.out_h);
+      } else {
+        if (slot_row < 0) continue;
+        dst = reinterpret_cast<uint4*>((isk ? a.pool.k : a.pool.v) + slot_row + h * a.pool.stride_h);
       }
+      dst[pa] = pack8(x[0]);
+      dst[pb] = pack8(x[1]);
     }
   }
 }
 
-// Warps per token: enough of them for every SM to hold about 32 while a token
-// has heads to share out, else at least eight groups of heads each, so that
-// the token's sines and cosines are computed few times.
-int token_parts(int64_t T, int groups) {
-  const int64_t want = (static_cast<int64_t>(kSms) * 32 + T - 1) / T;
-  const int64_t least = (groups + 7) / 8;
-  int64_t p = want > least ? want : least;
-  return static_cast<int>(p < groups ? p : groups);
+// Warps per token: enough of them for every SM to hold 28 while a token has
+// items to share out; with many tokens one warp takes a token whole, so that its
+// sines and cosines are computed once.
+int token_parts(int64_t T, int items) {
+  const int64_t p = (static_cast<int64_t>(kSms) * 28 + T - 1) / T;
+  return static_cast<int>(p < items ? p : items);
 }
 
 Rows rows_of(const tm_tensor* in, const tm_tensor* out, const void* w) {
@@ -301,16 +312,19 @@ void set_rope(TokenArgs* a, const tm_rope_freqs* r) {
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 tm_status launch_tokens(TokenArgs& a, int d, int cache, cudaStream_t stream) {
-  const int rpw = 256 / d;
-  const int groups = (a.hq + a.hk + a.hv + rpw - 1) / rpw;
-  a.parts = token_parts(a.T, groups);
+  const int rpw = 512 / d;
+  a.parts = token_parts(a.T, (a.hq + rpw - 1) / rpw + (a.hk + rpw - 1) / rpw + (a.hv + rpw - 1) / rpw);
   const int64_t blocks = (a.T * a.parts + kTokenWarps - 1) / kTokenWarps;
   if (blocks > 0x7fffffff) return TM_ERR_UNSUPPORTED;
   const DevErr err{device_error_word()};
   if (err.word == nullptr) return cuda_fail(static_cast<int>(cudaErrorInvalidSymbol));
-  auto kernel = cache == kCacheI8 ? (d == 128 ? token_kernel<128, kCacheI8> : token_kernel<64, kCacheI8>)
-                : cache == kCacheF16 ? (d == 128 ? token_kernel<128, kCacheF16> : token_kernel<64, kCacheF16>)
-                                     : (d == 128 ? token_kernel<128, kNoCache> : token_kernel<64, kNoCache>);
+  const bool norm = a.q.weight != nullptr || a.k.weight != nullptr;
+  auto kernel = norm ? (cache == kCacheI8 ? (d == 128 ? token_kernel<128, kCacheI8, true> : token_kernel<64, kCacheI8, true>)
+                        : cache == kCacheF16 ? (d == 128 ? token_kernel<128, kCacheF16, true> : token_kernel<64, kCacheF16, true>)
+                                             : (d == 128 ? token_kernel<128, kNoCache, true> : token_kernel<64, kNoCache, true>))
+                     : (cache == kCacheI8 ? (d == 128 ? token_kernel<128, kCacheI8, false> : token_kernel<64, kCacheI8, false>)
+                        : cache == kCacheF16 ? (d == 128 ? token_kernel<128, kCacheF16, false> : token_kernel<64, kCacheF16, false>)
+                                             : (d == 128 ? token_kernel<128, kNoCache, false> : token_kernel<64, kNoCache, false>));
   kernel<<<static_cast<unsigned>(blocks), kTokenWarps * 32, 0, stream>>>(a, err);
   return check_cuda(cudaGetLastError());
 }
