@@ -78,7 +78,7 @@ enum { kNoCache = 0, kCacheF16 = 1, kCacheI8 = 2 };
 // one.  So the rotation needs no shuffles; the norm's sum takes log2(D / 16).
 // U items are loaded before the first is used, to keep loads in flight.
 template <int D, int CACHE, bool NORM>
-__global__ void __launch_bounds__(kTokenWarps * 32) token_kernel(const __grid_constant__ TokenArgs a, DevErr err) {
+__global__ void __launch_bounds__(kTokenWarps * 32, 6) token_kernel(const __grid_constant__ TokenArgs a, DevErr err) {
   constexpr int LPR = D / 16;         // lanes of a head
   constexpr int RPW = 32 / LPR;       // heads of an item
   constexpr int U = 2;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32) token_kernel(const __grid_co
           for (int e = 0; e < 8; ++e) ss += x[0][e] * x[0][e] + x[1][e] * x[1][e];
 #pragma unroll
           for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+          const float inv = rsqrtf(ss * (1.0f / D) + a.eps);      // within 2^-22
           float wf[8];
           unpack8(__ldg(reinterpret_cast<const uint4*>(w) + pa), wf);
 #pragma unroll
@@ -243,11 +243,35 @@ __global__ void __launch_bounds__(kTokenWarps * 32) token_kernel(const __grid_co
           const float s = __half2float(s16);
           uint32_t c[2][2] = {{0, 0}, {0, 0}};
           if (s != 0.f) {
+            // x * (1 / s) is within 2^-22 of the quotient, relative, so its nearest integer is the quotient's
+            // unless it lies that close to the middle between two: then divide
+            const float by = __frcp_rn(s);
+            bool near = false;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              int v = __float2int_rn(__fdiv_rn(x[e >> 3][e & 7], s));
-              v = max(-127, min(127, v));
-              c[e >> 3][(e >> 2) & 1] |= static_cast<uint32_t>(v & 255) << (8 * (e & 3));
+            for (int p = 0; p < 2; ++p) {
+              uint32_t n[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float r = fminf(fmaxf(x[p][e] * by, -127.0f), 127.0f);
+                const float t = r + 12582912.0f;      // 1.5 * 2^23: the nearest integer, ties to even, in the low bits
+                near = near || fabsf(r - (t - 12582912.0f)) > 0.4999f;
+                n[e] = __float_as_uint(t);
+              }
+#pragma unroll
+              for (int e = 0; e < 8; e += 4)
+                c[p][e >> 2] = __byte_perm(__byte_perm(n[e], n[e + 1], 0x0040), __byte_perm(n[e + 2], n[e + 3], 0x0040),
+                                           0x5410);
+            }
+            if (near) {
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                c[p][0] = c[p][1] = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int v = max(-127, min(127, __float2int_rn(__fdiv_rn(x[p][e], s))));
+                  c[p][e >> 2] |= static_cast<uint32_t>(v & 255) << (8 * (e & 3));
+                }
+              }
             }
           }
           uint8_t* row = (isk ? a.pool.k : a.pool.v) + slot_row + h * a.pool.stride_h;
