@@ -612,8 +612,7 @@ tm_status tm_kv_gather(const tm_paged_kv* cache, const int32_t* table, int64_t t
  * by the whole batch) and own position j of its sequence iff j < kv_lens[b]
  * and (not causal or j <= i + kv_lens[b] - n_b).  One softmax runs over both:
  *   out = fp16( sum_j softmax_j(q . k_j / sqrt(d)) v_j )
- * fp32 scores, statistics and sums; for the P.V product P is rounded to fp16,
- * and V of INT8 pages may be (fp16(code * scale), as tm_kv_gather gives it).  A
+ * fp32 scores, statistics and sums; P rounded to fp16 for the P.V product.  A
  * row that sees nothing is 0; rows behind the last sequence are left as they
  * were.  Values at visible and causally hidden positions below kv_lens[b] must
  * be finite; the rest of a page is never used.

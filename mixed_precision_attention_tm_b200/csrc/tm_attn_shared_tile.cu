@@ -16,11 +16,11 @@
 // that nothing behind a sequence's end is ever used.
 //
 // INT8 pages: the copies bring the codes, which two more warpgroups (one
-// for K, one for V) turn into fp16 in place.  K stays codes (exactly) and a key's scale multiplies its scores in
-// fp32; V becomes fp16(code * scale), the value that tm_kv_gather gives: its one
-// rounding is of the size of P's, and carrying V's scale in P instead would take
-// a second pass of 128-byte shared-memory reads through the softmax and fp16's
-// range from the weights.
+// for K, one for V) turn into fp16 in place, exactly: K stays codes, V is code
+// times the largest power of two in its scale.  A key's K scale multiplies its
+// scores in fp32 and the rest of its V scale (between 1 and 2) its weight before
+// that is rounded, so that the scales add no rounding.  (V rounded to fp16
+// (code * scale) is a shared-memory pass less, and 1.2 times the error.)
 //
 // The prefix's work is one line of key tiles (row block by row block) cut into
 // equal pieces, one for each CTA, so that all SMs finish together; a CTA whose
@@ -38,8 +38,10 @@ namespace tmk {
 namespace {
 
 // 2^kPOffset is the largest weight when the reference is the maximum; scores
-// up to 2^kLazy above it are left alone: 2^15 at most, inside fp16.
-constexpr float kLazy = 15.0f - kPOffset;
+// up to 2^kLazyTile above it are left alone: 2^15 at most, inside fp16, with what
+// INT8 V scales multiply in (less than 2).
+template <bool INT8>
+constexpr float kLazyTile = (INT8 ? 14.0f : 15.0f) - kPOffset;
 
 // Of every 8 pairs of exponentials, how many run on the FMA pipe: the special
 // function unit alone takes as long as the MMAs of a tile.
@@ -54,12 +56,13 @@ struct CfgT {
   static constexpr int HALF = 128 * 128;               // one 64-column slab of a tile
   static constexpr int SLOT = BN * D * 2;              // an fp16 K or V tile
   static constexpr int NSLOT = 131072 / SLOT;          // 4 (d = 128) or 8 (d = 64)
-  static constexpr int STAGES = NSLOT / 2 + 1;         // of K scales
+  static constexpr int STAGES = NSLOT / 2 + 1;         // of scales
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int OFF_SLOT = 2 * Q_BYTES;
-  static constexpr int OFF_SCALE = OFF_SLOT + NSLOT * SLOT;      // [STAGES][128] K scales
-  static constexpr int OFF_STAGE = OFF_SCALE + STAGES * 128 * 4;  // 4 KB for each softmax warp: results on their way out
-  static constexpr int OFF_BAR = OFF_STAGE + 8 * 4096;
+  static constexpr int OFF_SCALE = OFF_SLOT + NSLOT * SLOT;         // INT8: [STAGES][2][128] scales
+  static constexpr int OUT_COLS = INT8 ? 16 : 32;                   // of results on their way out, 32 rows of each softmax warp
+  static constexpr int OFF_OUT = OFF_SCALE + (INT8 ? STAGES * 256 * 4 : 0);
+  static constexpr int OFF_BAR = OFF_OUT + 8 * 32 * OUT_COLS * 4;
   static constexpr int SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t IDESC_S = idesc_f16(BM, 64, false);
   static constexpr uint32_t IDESC_PV = idesc_f16(BM, D, true);
@@ -410,33 +413,42 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
     regs_dec<C::CONVERT_REGS>();
     const int v = (warp - 12) >> 2;
     const int r = threadIdx.x & 127;
-    const __half* const scale_of = (v ? a.pool.vs : a.pool.ks);
     uint32_t i = v;
     while (next_segment(u, sg)) {
       const int nj = sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
       // this row's page and scale, loaded two and one key tiles ahead
       auto entry_of = [&](int j) { return j < nj ? entry_at(sg, sg.key0 + j * 128 + r) : -1; };
-      auto scale_at = [&](int j, int32_t page) -> __half {
-        if (!page_ok(page, a.pool.num_pages)) return __float2half(0.f);
-        return scale_of[page * a.pool.sstride_page + ((sg.key0 + j * 128 + r) & page_mask) * a.pool.sstride_t +
-                        sg.kvh * a.pool.sstride_h];
+      auto scales_at = [&](int j, int32_t page, __half& ks, __half& vs) {
+        ks = vs = __float2half(0.f);
+        if (!page_ok(page, a.pool.num_pages)) return;
+        const int64_t at = page * a.pool.sstride_page + ((sg.key0 + j * 128 + r) & page_mask) * a.pool.sstride_t +
+                           sg.kvh * a.pool.sstride_h;
+        if (v == 0) ks = a.pool.ks[at];
+        vs = a.pool.vs[at];
       };
       int32_t entry = entry_of(0);
-      __half next = scale_at(0, entry);
+      __half ks, vs, next_ks, next_vs;
+      scales_at(0, entry, next_ks, next_vs);
       entry = entry_of(1);
       for (int j = 0; j < nj; ++j, i += 2) {
-        const __half scale = next;
-        next = scale_at(j + 1, entry);
+        ks = next_ks;
+        vs = next_vs;
+        scales_at(j + 1, entry, next_ks, next_vs);
         entry = entry_of(j + 2);
         {
           const uint32_t slot = i % C::NSLOT;
           mbar_wait_warp(bar(T_CODES + slot), (i / C::NSLOT) & 1, err, abort_flag);
           const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT;
-          // K's scales outlive its slot: the softmax reads those of key tile j until P(2 j + 1).  With one stage more
+          // The scales outlive K's slot: the softmax reads those of key tile j until P(2 j + 1).  With one stage more
           // than the ring has key tiles, the next tile in this stage lands behind a release of key tile j + 1, whose
           // last S is issued behind P.V(2 j + 1).
-          if (v == 0) scales[((i / 2) % C::STAGES) * 128 + r] = __half2float(scale);
-          const __half2 by = __half2half2(v ? scale : __float2half(1.f));
+          const uint32_t bits = __float_as_uint(__half2float(vs));
+          if (v == 0) {
+            float* sc = scales + ((i / 2) % C::STAGES) * 256 + r;
+            sc[0] = __half2float(ks);
+            sc[128] = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);      // 1 <= |f| < 2; of a zero scale: 1
+          }
+          const __half2 by = __half2half2(__float2half(v ? __uint_as_float(bits & 0x7f800000u) : 1.f));
           auto widen = [&](uint4 c, uint32_t at, int q) {      // 16 codes to pieces 2 q and 2 q + 1 of a row
             const uint32_t x[4] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u};
             sts128(at + (((2 * q) ^ (r & 7)) << 4),
@@ -636,7 +648,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           for (int e = 0; e < HN; ++e) x[e] = __uint_as_float(v[e]);
         }
         if (INT8) {
-          const float* sc = scales + ((n + (c >> 1)) % C::STAGES) * 128 + HN * sl;
+          const float* sc = scales + ((n + (c >> 1)) % C::STAGES) * 256 + HN * sl;
 #pragma unroll
           for (int e = 0; e < HN; e += 4) {
             const float4 k4 = *reinterpret_cast<const float4*>(sc + e);
@@ -653,7 +665,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         float alpha = 1.f;
         if (nv > 0) {
           const float mt = row_max<HN>(x) * cs;
-          if (mt > m_used + kLazy) {
+          if (mt > m_used + kLazyTile<INT8>) {
             alpha = ex2_approx(m_used - mt);
             m_used = mt;
           }
@@ -676,6 +688,10 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
             p1 = ex2_approx(y1);
           }
           acc2[(e >> 1) & 3] = f2add(acc2[(e >> 1) & 3], f2pack(p0, p1));
+          if (INT8) {
+            const float2 f = *reinterpret_cast<const float2*>(scales + ((n + (c >> 1)) % C::STAGES) * 256 + 128 + HN * sl + e);
+            f2unpack(f2mul(f2pack(p0, p1), f2pack(f.x, f.y)), p0, p1);
+          }
           pk[e >> 1] = pack_half2(p0, p1);
         }
         {
@@ -729,13 +745,17 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       if (row_ok && !direct) a.ml[sg.slot * total + idx] = make_float2(m_used, l);
       const float inv = !direct ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
       if (nt > 0 || direct) {
-        // 32 columns of the warp's 32 rows at a time through shared memory, so that a store instruction writes
-        // four rows' whole 128-byte lines instead of 32 rows' halves of sectors
-        const uint32_t stage = sbase + C::OFF_STAGE + warp * 4096;
+        // OUT_COLS columns of the warp's 32 rows at a time through shared memory, so that a store instruction writes
+        // whole lines (or halves) of a few rows instead of 32 rows' halves of sectors
+        constexpr int PR = C::OUT_COLS / 4, RPI = 32 / PR;        // 16-byte pieces of a row, rows of an instruction
+        const uint32_t stage = sbase + C::OFF_OUT + warp * (32 * C::OUT_COLS * 4);
+        auto place = [&](int row, int e) {
+          return stage + row * (PR * 16) + ((PR == 8 ? e ^ (row & 7) : e ^ ((row >> 1) & 3)) << 4);
+        };
         const int64_t mine = row_ok ? (direct ? tok * a.o_t + head * a.o_h : (sg.slot * total + idx) * D) : -1;
-        int64_t at[8];        // where rows lane / 8 + 4 i go
+        int64_t at[PR];       // where rows lane / PR + RPI i go
 #pragma unroll
-        for (int i = 0; i < 8; ++i) at[i] = __shfl_sync(0xffffffffu, mine, 4 * i + (lane >> 3));
+        for (int i = 0; i < PR; ++i) at[i] = __shfl_sync(0xffffffffu, mine, RPI * i + lane / PR);
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
@@ -747,26 +767,31 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            sts128(stage + lane * 128 + ((e ^ (lane & 7)) << 4),
-                   make_uint4(__float_as_uint(__uint_as_float(o[4 * e]) * inv),
-                              __float_as_uint(__uint_as_float(o[4 * e + 1]) * inv),
-                              __float_as_uint(__uint_as_float(o[4 * e + 2]) * inv),
-                              __float_as_uint(__uint_as_float(o[4 * e + 3]) * inv)));
-          __syncwarp();
+          for (int hh = 0; hh < 32 / C::OUT_COLS; ++hh) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = 4 * i + (lane >> 3), e = lane & 7;
-            const uint4 v = lds128(stage + row * 128 + ((e ^ (row & 7)) << 4));
-            if (at[i] < 0) continue;
-            if (direct)
-              *reinterpret_cast<uint2*>(a.out + at[i] + q * 32 + e * 4) =
-                  make_uint2(pack_half2(__uint_as_float(v.x), __uint_as_float(v.y)),
-                             pack_half2(__uint_as_float(v.z), __uint_as_float(v.w)));
-            else
-              *reinterpret_cast<uint4*>(a.o + at[i] + q * 32 + e * 4) = v;
+            for (int e = 0; e < PR; ++e) {
+              const uint32_t* x = o + hh * C::OUT_COLS + 4 * e;
+              sts128(place(lane, e), make_uint4(__float_as_uint(__uint_as_float(x[0]) * inv),
+                                                __float_as_uint(__uint_as_float(x[1]) * inv),
+                                                __float_as_uint(__uint_as_float(x[2]) * inv),
+                                                __float_as_uint(__uint_as_float(x[3]) * inv)));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < PR; ++i) {
+              const int row = RPI * i + lane / PR, e = lane % PR;
+              const uint4 v = lds128(place(row, e));
+              if (at[i] < 0) continue;
+              const int col = q * 32 + hh * C::OUT_COLS + e * 4;
+              if (direct)
+                *reinterpret_cast<uint2*>(a.out + at[i] + col) =
+                    make_uint2(pack_half2(__uint_as_float(v.x), __uint_as_float(v.y)),
+                               pack_half2(__uint_as_float(v.z), __uint_as_float(v.w)));
+              else
+                *reinterpret_cast<uint4*>(a.o + at[i] + col) = v;
+            }
+            __syncwarp();         // tensor-memory loads and the stage are the whole warp's
           }
-          __syncwarp();           // tensor-memory loads and the stage are the whole warp's
         }
         tc_fence_before();      // these reads of O come before the next segment's first P.V
       }

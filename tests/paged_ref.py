@@ -80,14 +80,13 @@ def rows_of(pool, pages, n):
     return pool[idx].flatten(0, 1)[:n] if idx else pool[:0].flatten(0, 1)
 
 
-def attention(q, pools, table, kv_lens, new, prefix_pages=(), prefix_len=0, causal=True,
-              int8=False):
+def attention(q, pools, table, kv_lens, new, prefix_pages=(), prefix_len=0, causal=True):
     """(out, error allowed) [T, Hq, d], 64 bits.  pools: float64 K and V pages.
 
     Error: a score sums d products (2^-24 of their absolute sum each) and is
     scaled; a weight is its exponential (to 2^-18), rounded to fp16 (2^-11, or 2^-31 of the
     largest below fp16's normal range); the sums run in fp32 in any order; the
-    result is rounded once.  int8: so is each value of V, code times scale."""
+    result is rounded once."""
     kp, vp = pools
     T, hq, d = q.shape
     hkv = kp.shape[2]
@@ -116,8 +115,7 @@ def attention(q, pools, table, kv_lens, new, prefix_pages=(), prefix_len=0, caus
             ds = (qh.abs() @ kh.abs().T / math.sqrt(d)).masked_fill(~seen, 0).amax(-1, keepdim=True)
             ds = ds * (d + 8) * 2.0 ** -24 + 2.0 ** -21
             steps = len(j) * 2.0 ** -24 + 2.0 ** -17      # the exponential counts in the weight and in their sum
-            tol[t0:t0 + n, h] += (total * (HALF * (2 if int8 else 1) + steps) + (total + out[t0:t0 + n, h].abs()) * 2 * ds
-                                  + out[t0:t0 + n, h].abs() * HALF + len(j) * 2.0 ** -31 * vh.abs().amax(0)
-                                  + (TINY if int8 else 0))
+            tol[t0:t0 + n, h] += (total * (HALF + steps) + (total + out[t0:t0 + n, h].abs()) * 2 * ds
+                                  + out[t0:t0 + n, h].abs() * HALF + len(j) * 2.0 ** -31 * vh.abs().amax(0))
         t0 += n
     return out, tol

@@ -275,7 +275,7 @@ def attend(seed, lens, new, prefix, d, page, hq, hkv, int8, order="page", causal
     ops.attn_shared_prefix(q, kv, table, i32(lens), **args)
     ok()
     want, tol = ref.attention(q[:T], values(kv), table.cpu(), lens, new,
-                              [] if shared is None else shared.cpu().tolist(), prefix, causal, int8)
+                              [] if shared is None else shared.cpu().tolist(), prefix, causal)
     within(out[:T], want, tol)
     assert bool((out[T:] == 3.0).all())
     return q, kv, table, shared, out
@@ -399,7 +399,7 @@ def test_two_graphs_with_their_workspaces_and_streams():
         for s in state:
             got = s["out"].clone()
             want, tol = ref.attention(s["qr"], values(s["kv"]), s["table"].cpu(), s["lens"].tolist(), [1] * n,
-                                      s["shared"].tolist(), prefix, int8=s["kv"].int8)
+                                      s["shared"].tolist(), prefix)
             within(got, want, tol)
     ok()
     graphs.clear()
