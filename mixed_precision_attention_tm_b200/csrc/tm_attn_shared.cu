@@ -16,11 +16,11 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t ba
   SharedPlan p{};
   p.group = Hq / Hkv;
   const int64_t own_packed = max_seqlen * p.group, pre_packed = T * p.group;
-  p.own_tile = own_packed > kSplitRowsOwn;
-  p.pre_tile = prefix_len > 0 && pre_packed > kSplitRowsPrefix;
+  const int64_t own_units = ceil_div(max_kv_len, 128), pre_units = ceil_div(prefix_len, 128);
+  p.own_tile = own_on_tiles(own_packed, own_units);
+  p.pre_tile = prefix_on_tiles(ceil_div(pre_packed, 16) * Hkv, ceil_div(pre_packed, 256) * Hkv, pre_units);
   const int64_t own_rows = ceil_div(own_packed, p.own_tile ? 256 : 16);
   const int64_t pre_rows = ceil_div(pre_packed, p.pre_tile ? 256 : 16);
-  const int64_t own_units = ceil_div(max_kv_len, 128), pre_units = ceil_div(prefix_len, 128);
   p.own_rows = static_cast<int>(own_rows);
   p.pre_rows = static_cast<int>(pre_rows);
   // split kernel: pieces small enough for five CTAs per SM, so that sequences of different lengths (known on the

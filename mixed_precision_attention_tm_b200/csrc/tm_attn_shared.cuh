@@ -27,9 +27,19 @@ constexpr int kSmsB200 = 148;
 // values fp16 holds) multiplied in, below fp16's 65504.
 constexpr float kPOffset = 6.0f;
 
-// Rows (of a sequence, of the batch) up to which the split-key kernel takes
-// the own tokens or the prefix; more rows go to the tile kernel.
-constexpr int kSplitRowsOwn = 64, kSplitRowsPrefix = 16;
+// Which kernel takes the prefix, and which the own tokens.  The split-key
+// kernel costs about 0.008 us for each 16-row block and key tile of 128; the tile
+// kernel starts about 9 us later and costs 0.013 us for each 256-row block and key tile.
+// Measured (32 query heads over 8, 32 tokens of single rows, fp16): behind 1024
+// shared positions 15.8 us (split) and 19.4 us (tile), behind 8192 42.0 and 24.9 us.
+constexpr int64_t kTileStart = 1000;      // in 16-row blocks and key tiles
+constexpr bool prefix_on_tiles(int64_t blocks16, int64_t blocks256, int64_t key_tiles) {
+  return 2 * blocks16 * key_tiles > 2 * kTileStart + 3 * blocks256 * key_tiles;
+}
+// A sequence's packed rows: a tile of few rows is mostly empty (60 sequences of
+// 64 rows over 600 keys: 104 us split, 95 us on tiles; over 150 keys 67 and 70
+// us; of 32 rows 105 and 149 us).
+constexpr bool own_on_tiles(int64_t rows, int64_t key_tiles) { return rows > 64 || (rows > 48 && key_tiles > 4); }
 constexpr int kMostSplits = 30;
 // Key tiles that a row block's start and end cost a CTA of the tile kernel (about 6 us at 1.9 us a tile).
 constexpr int kSplitBlockTiles = 3;

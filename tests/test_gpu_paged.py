@@ -293,6 +293,27 @@ def test_attention(d, page, hq, hkv, int8, order, lens, new, prefix):
     attend(20, lens, new, prefix, d, page, hq, hkv, int8, order, tail=2)
 
 
+@pytest.mark.parametrize("d,page,hq,hkv,int8,order", CACHES)
+@pytest.mark.parametrize("prefix", [2300, 2304])
+def test_attention_on_tiles(d, page, hq, hkv, int8, order, prefix):
+    """Rows and keys enough for the tile kernel, on both sides of the prefix's end; rows behind the last sequence."""
+    attend(43, [301, 100, 4, 0], [300, 100, 1, 0], prefix, d, page, hq, hkv, int8, order, tail=3)
+
+
+@pytest.mark.parametrize("hq,hkv", [(28, 4), (6, 2), (8, 2)])
+@pytest.mark.parametrize("int8", [False, True])
+def test_attention_on_tiles_groups(hq, hkv, int8):
+    """Query heads per K/V head that do and do not divide a tile's 128 rows."""
+    attend(44, [200, 150], [200, 97], 1900, 128, 32, hq, hkv, int8)
+    attend(45, [200, 150], [200, 97], 1900, 64, 64, hq, hkv, int8, causal=False)
+
+
+@pytest.mark.parametrize("d,int8", [(64, False), (128, True)])
+def test_attention_in_pieces_of_the_line(d, int8):
+    """As many row blocks as SMs, whose key tiles are cut without regard to the blocks."""
+    attend(46, [900, 690, 3], [900, 690, 1], 2700, d, 128, 16, 16, int8)
+
+
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (16, 1), (28, 4), (24, 8), (64, 2), (40, 2)])
 @pytest.mark.parametrize("int8", [False, True])
 def test_attention_groups(hq, hkv, int8):
@@ -321,9 +342,10 @@ def test_attention_flat_and_peaked(scale):
     attend(26, [200, 90], [3, 1], 400, 64, 16, 4, 2, False, scale=scale)
 
 
-def test_attention_ignores_what_no_row_sees():
+@pytest.mark.parametrize("prefix", [150, 2500])        # on the split-key kernel, on the tile kernel
+def test_attention_ignores_what_no_row_sees(prefix):
     """NaN and infinities in unused slots, unused pages and (as keys) at causally hidden positions change nothing."""
-    lens, new, prefix, page = [70, 21, 140], [1, 1, 130], 150, 64
+    lens, new, prefix, page = [70, 21, 140], [1, 1, 130], prefix, 64
     g = gen(27)
     table, shared, total = make_table(27, lens, page, extra=prefix)
     q = randn(g, sum(new), 8, 128)
@@ -342,20 +364,26 @@ def test_attention_ignores_what_no_row_sees():
         assert torch.equal(got, want)
 
 
-def test_attention_bad_pages_are_reported_and_not_read():
+@pytest.mark.parametrize("bad", ["past the pool", "negative", "in the prefix"])
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("rows,prefix", [(1, 64), (100, 64), (100, 3000)])
+def test_attention_bad_pages_are_reported_and_not_read(rows, prefix, int8, bad):
     g = gen(28)
-    table, shared, total = make_table(28, [100, 40], 16, extra=64)
-    kv = make_pool(g, total, 16, 2, 64, False)
-    q = randn(g, 2, 4, 64)
-    table[0, 3] = total
-    args = dict(prefix_pages=shared, prefix_len=64)
-    out = ops.attn_shared_prefix(q, kv, table, i32([100, 40]), **args)
+    table, shared, total = make_table(28, [100, 140], 16, extra=prefix)
+    kv = make_pool(g, total, 16, 2, 64, int8)
+    q = randn(g, 2 * rows, 8, 64)
+    args = dict(prefix_pages=shared, prefix_len=prefix)
+    where = shared[1:2] if bad == "in the prefix" else table[0, 3:4]
+    old = where.clone()
+    where.fill_(total if bad == "past the pool" else -3)
+    out = ops.attn_shared_prefix(q, kv, table, i32([100, 140]), **args)
     torch.cuda.synchronize()
     assert ops.get_device_error() == ops.TM_ERR_INVALID_ARG
-    table[0, 3] = 0
-    good = ops.attn_shared_prefix(q, kv, table, i32([100, 40]), **args)
+    where.copy_(old)
+    good = ops.attn_shared_prefix(q, kv, table, i32([100, 140]), **args)
     ok()
-    assert torch.equal(out[1], good[1])
+    if bad != "in the prefix":
+        assert torch.equal(out[rows:], good[rows:])      # the other sequence does not see that page
 
 
 def test_two_graphs_with_their_workspaces_and_streams():
@@ -470,6 +498,6 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.parametrize("d,int8", [(128, False), (64, True), (128, True), (64, False)])
-def test_attention_pieces_across_row_blocks(d, int8):
-    """More key tiles of the prefix than SMs, in pieces that end inside row blocks; ragged own rows of several tiles."""
+def test_attention_pieces_of_row_blocks(d, int8):
+    """More key tiles of the prefix than SMs; ragged own rows of several tiles."""
     attend(41, [260, 90, 2], [110, 90, 1], 2500, d, 32, 16, 4, int8)
