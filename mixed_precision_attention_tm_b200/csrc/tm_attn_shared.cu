@@ -16,8 +16,14 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t ba
   SharedPlan p{};
   p.group = Hq / Hkv;
   const int64_t own_packed = max_seqlen * p.group, pre_packed = T * p.group;
-  const int64_t own_units = ceil_div(max_kv_len, 128), pre_units = ceil_div(prefix_len, 128);
+  int64_t own_units = ceil_div(max_kv_len, 128), pre_units = ceil_div(prefix_len, 128);
   p.own_tile = own_on_tiles(own_packed, own_units);
+  if (p.own_tile && prefix_len + max_kv_len < (1 << 30) &&
+      prefix_folded(batch * ceil_div(own_packed, 256) * Hkv, ceil_div(pre_packed, 256) * Hkv, pre_units)) {
+    p.fold = static_cast<int>(pre_units);
+    own_units += pre_units;
+    pre_units = 0;
+  }
   p.pre_tile = prefix_on_tiles(ceil_div(pre_packed, 16) * Hkv, ceil_div(pre_packed, 256) * Hkv, pre_units);
   const int64_t own_rows = ceil_div(own_packed, p.own_tile ? 256 : 16);
   const int64_t pre_rows = ceil_div(pre_packed, p.pre_tile ? 256 : 16);
@@ -66,8 +72,19 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t ba
     p.pre_chunk = static_cast<int>((c < 1 ? 1 : c) * 128);
     p.pre_splits = static_cast<int>(ceil_div(pre_units, c < 1 ? 1 : c));
   }
-  int64_t c = p.own_tile ? ceil_div(batch * own_rows * Hkv * own_units, 2 * kSmsB200) : chunk;
-  if (p.own_tile && c < 4) c = 4;
+  int64_t c = chunk;
+  if (p.own_tile) {
+    // as many splits as end soonest: waves of items, each its key tiles and a start worth kItemTiles more
+    const int64_t items = batch * own_rows * Hkv;
+    int64_t best = 0;
+    for (int64_t s = 1; s <= kMostSplits && s <= own_units; ++s) {
+      const int64_t cost = ceil_div(items * s, kSmsB200) * (ceil_div(own_units, s) + kItemTiles) + (s > 1 ? kItemTiles : 0);
+      if (best == 0 || cost < best) {
+        best = cost;
+        c = ceil_div(own_units, s);
+      }
+    }
+  }
   if (c < ceil_div(own_units, kMostSplits)) c = ceil_div(own_units, kMostSplits);
   if (c < 1) c = 1;
   p.own_chunk = static_cast<int>(c * 128);

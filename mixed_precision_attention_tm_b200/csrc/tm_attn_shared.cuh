@@ -40,6 +40,14 @@ constexpr bool prefix_on_tiles(int64_t blocks16, int64_t blocks256, int64_t key_
 // 64 rows over 600 keys: 104 us split, 95 us on tiles; over 150 keys 67 and 70
 // us; of 32 rows 105 and 149 us).
 constexpr bool own_on_tiles(int64_t rows, int64_t key_tiles) { return rows > 64 || (rows > 48 && key_tiles > 4); }
+// A short prefix is multiplied by every row block of the own tokens instead of
+// once for the packed batch, which costs the tiles that packing saves and spares a
+// pass, its results and the join (about 20 us, 1200 row blocks and key tiles: measured equal at 1248).
+constexpr bool prefix_folded(int64_t own_blocks, int64_t packed_blocks, int64_t key_tiles) {
+  return (own_blocks - packed_blocks) * key_tiles < 1200;
+}
+// Key tiles that an item of own tokens costs besides its own (first copies, way out), and a join.
+constexpr int kItemTiles = 4;
 constexpr int kMostSplits = 30;
 // Key tiles that a row block's start and end cost a CTA of the tile kernel (about 6 us at 1.9 us a tile).
 constexpr int kSplitBlockTiles = 3;
@@ -50,6 +58,7 @@ struct SharedPlan {
   int own_rows, pre_rows;     // row blocks per sequence, of the batch
   int own_splits, pre_splits; // most results of a row
   int own_chunk;              // keys per split
+  int fold;                   // key tiles of the prefix that the own tokens' row blocks go through first (no prefix results)
   int pre_chunk;              // the same; on the tile kernel: key tiles per CTA
   int pre_tiles, pre_ctas;    // tile kernel: key tiles of the prefix, CTAs
   int pre_pieces;             // tile kernel: pieces of a row block, 0: pieces of the whole line

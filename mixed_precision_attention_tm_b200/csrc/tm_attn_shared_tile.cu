@@ -44,11 +44,12 @@ template <bool INT8>
 constexpr float kLazyTile = (INT8 ? 14.0f : 15.0f) - kPOffset;
 
 // Of every 8 pairs of exponentials, how many run on the FMA pipe: the special
-// function unit alone takes as long as the MMAs of a tile.
-#ifndef TM_FMA_PAIRS
-#define TM_FMA_PAIRS 3
-#endif
-constexpr int kFmaPairs = TM_FMA_PAIRS;
+// function unit alone takes as long as the MMAs of a tile.  A 64-key step of both
+// tiles in SM cycles with 0, 2, 3 and 4: 1753, 1546, 1552, 1630 (fp16).  With
+// INT8 pages the conversion warps want the same pipes (1024 rows behind 16384
+// positions: 378 us with 2, 385 us with 3).
+template <bool INT8>
+constexpr int kFmaPairs = INT8 ? 2 : 3;
 
 template <int D, bool INT8>
 struct CfgT {
@@ -100,8 +101,9 @@ enum : int { NB_P = 1, NB_KV = 5, NB_TURN = 7, NB_CVT = 9 };
 struct Segment {
   int kvh, b, slot, rows;     // rows of the block: 1 .. 256
   int row0, start;            // first packed row (of the batch or the sequence), first token
-  int key0, lk;               // first key, keys that exist
-  int hidden;                 // own, causal: token i of the sequence sees keys below hidden + i
+  int key0;                   // first key: of the prefix, or of the prefix's whole tiles (where they are folded in) and own tokens behind them
+  int lk;                     // own keys (of the prefix: its length)
+  int hidden;                 // own, causal: token i of the sequence sees own keys below hidden + i
   int nj[2];                  // key tiles that each query tile sees
 };
 
@@ -141,9 +143,9 @@ struct TileMaps {
   PageMaps kv;
 };
 
-template <int D, bool INT8>
+template <int D, bool INT8, bool prefix>
 __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
-    tile_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ TileMaps maps, int prefix, DevErr err) {
+    tile_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ TileMaps maps, DevErr err) {
   using C = CfgT<D, INT8>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = smem_u32(smem_raw);
@@ -160,8 +162,13 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
 
   pdl_launch_dependents();
 
+  // Own tokens with the prefix folded in: keys below `fold` are the prefix's, own key k is key fold + k (a whole tile's
+  // boundary).
+  const int fold = prefix ? 1 << 30 : p.fold * 128;
+
   // ---- this CTA's segments, walked by every role alike
-  int unit = 0, unit_end = 1;         // prefix: key tiles of the line
+  // prefix: key tiles of the line; own: items (a row block against a split), every gridDim.x-th
+  int unit = blockIdx.x, unit_end = p.own_splits * a.batch * p.own_rows * H;
   if (prefix) {
     if (p.pre_pieces > 0) {
       const int rb = static_cast<int>(blockIdx.x) / p.pre_pieces, piece = static_cast<int>(blockIdx.x) - rb * p.pre_pieces;
@@ -191,10 +198,9 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       if (s.rows > 128) s.nj[1] = count;
       return true;
     }
-    u = unit_end;
-    int item = blockIdx.x;
-    s.kvh = item % H;
-    item /= H;
+    int item = u / H;
+    s.kvh = u - item * H;
+    u += gridDim.x;
     const int per = a.batch * p.own_rows;
     const int split = item / per;
     item -= split * per;
@@ -217,12 +223,13 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       lk = static_cast<int>(a.max_kv);
     }
     s.hidden = lk - n + 1;
-    s.lk = max(0, min(s.key0 + p.own_chunk, lk));
+    s.lk = max(0, lk);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (s.rows <= 128 * t) continue;
       int seen = s.lk;
       if (a.causal) seen = min(seen, s.hidden + (s.row0 + min(s.rows, 128 * (t + 1)) - 1) / g);
+      seen = min(fold + max(seen, 0), s.key0 + p.own_chunk);
       s.nj[t] = seen > s.key0 ? (seen - s.key0 + 127) / 128 : 0;
     }
     return true;
@@ -231,13 +238,16 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
   // Page of key `key` of a segment: -1 behind its end, -2 where it cannot be used
   const int shift = a.pool.page_shift;
   const int page_mask = (1 << shift) - 1;
+  const int prefix_len = static_cast<int>(a.prefix_len);
+  auto place = [&](int key) { return key < fold ? key : key - fold; };                       // within prefix or sequence
+  auto keys_of = [&](const Segment& s, int key) { return key < fold ? prefix_len : s.lk; };  // how many there are
   auto entry_at = [&](const Segment& s, int key) -> int32_t {     // as the table has it
-    const int col = key >> shift;
-    if (key >= s.lk || (!prefix && col >= a.pt.cols)) return -1;
-    return __ldg(prefix ? a.prefix_pages + col : a.pt.table + s.b * a.pt.stride + col);
+    const int k = place(key), col = k >> shift;
+    if (k >= keys_of(s, key) || (key >= fold && col >= a.pt.cols)) return -1;
+    return __ldg(key < fold ? a.prefix_pages + col : a.pt.table + s.b * a.pt.stride + col);
   };
   auto page_at = [&](const Segment& s, int key) -> int32_t {
-    if (key >= s.lk) return -1;
+    if (place(key) >= keys_of(s, key)) return -1;
     const int32_t page = entry_at(s, key);
     return page_ok(page, a.pool.num_pages) ? page : -2;
   };
@@ -281,7 +291,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       if (lane == 0) mbar_arrive_expect_tx(bar(LANDED + slot), C::LOADED);
       __syncwarp();
       if (lane < boxes) {
-        const int32_t s0 = key & page_mask;
+        const int32_t s0 = place(key) & page_mask;
         const int32_t c1 = maps.kv.heads_inner ? sg.kvh : s0, c2 = maps.kv.heads_inner ? s0 : sg.kvh;
 #pragma unroll
         for (int hh = 0; hh < (INT8 ? 1 : D / 64); ++hh)
@@ -291,7 +301,8 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       __syncwarp();
     };
     // a ragged tile: row by row; the page of each run of 16 keys is in lane `run`
-    auto copy_rows = [&](const uint8_t* base, uint32_t slot, int32_t page, int key0) {
+    auto copy_rows = [&](const uint8_t* base, uint32_t slot, int32_t page, int tile_key) {
+      const int key0 = place(tile_key), end = keys_of(sg, tile_key);
       constexpr int ROW = D * (INT8 ? 1 : 2), PIECES = ROW / 16, RPI = 32 / PIECES;
       const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT + DST;
       const int c = lane % PIECES;
@@ -306,7 +317,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           const int r = 16 * run + rr;
           const uint32_t dst = INT8 && D == 64 ? tile + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)
                                                : tile + (c >> 3) * C::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-          const bool real = pg >= 0 && key + rr < sg.lk;
+          const bool real = pg >= 0 && key + rr < end;
           cp16(dst, real ? src + rr * a.pool.stride_t : base, real);
         }
       }
@@ -371,7 +382,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         const int32_t next = my_page(j + 1);
         if (page == -2) dev_error(err, TM_DEVERR_SEQLEN);
         const uint32_t i = 2 * n;
-        if (maps.kv.ok && key0 + 128 <= sg.lk && __all_sync(0xffffffffu, lane >= boxes || page >= 0)) {
+        if (maps.kv.ok && place(key0) + 128 <= keys_of(sg, key0) && __all_sync(0xffffffffu, lane >= boxes || page >= 0)) {
           const int key = key0 + lane * step;
           acquire(i);
           copy_boxes(&maps.kv.k, i % C::NSLOT, page, key);
@@ -421,7 +432,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       auto scales_at = [&](int j, int32_t page, __half& ks, __half& vs) {
         ks = vs = __float2half(0.f);
         if (!page_ok(page, a.pool.num_pages)) return;
-        const int64_t at = page * a.pool.sstride_page + ((sg.key0 + j * 128 + r) & page_mask) * a.pool.sstride_t +
+        const int64_t at = page * a.pool.sstride_page + (place(sg.key0 + j * 128 + r) & page_mask) * a.pool.sstride_t +
                            sg.kvh * a.pool.sstride_h;
         if (v == 0) ks = a.pool.ks[at];
         vs = a.pool.vs[at];
@@ -623,11 +634,10 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       const bool row_ok = pr < sg.rows;
       const int prow = sg.row0 + pr, tok_in = prow / g;
       const int tok = sg.start + tok_in, head = sg.kvh * g + prow - tok_in * g;
-      int lim = 0;
-      if (row_ok) {
-        lim = sg.lk;
-        if (!prefix && a.causal) lim = min(lim, sg.hidden + tok_in);
-      }
+      // keys below these are seen, in the prefix and behind it
+      const int lim_prefix = row_ok ? prefix_len : 0;
+      int lim_own = fold;
+      if (row_ok && !prefix) lim_own += max(0, a.causal ? min(sg.lk, sg.hidden + tok_in) : sg.lk);
       float m_used = -INFINITY, l = 0.f;
       // The two softmax warpgroups take turns at their exponentials: side by side they would slow each other down
       // into lockstep, and stores, waits and handoffs of both would leave the SM idle at the same time.
@@ -657,7 +667,8 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           }
         }
         const float cs = a.scale_log2;
-        const int nv = max(0, min(lim - sg.key0 - c * HN, HN));
+        const int key0 = sg.key0 + c * HN;
+        const int nv = max(0, min((key0 < fold ? lim_prefix : lim_own) - key0, HN));
         if (!__all_sync(0xffffffffu, nv == HN)) {
 #pragma unroll
           for (int e = 0; e < HN; ++e) x[e] = (e < nv) ? x[e] : -INFINITY;
@@ -679,7 +690,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         for (int e = 0; e < HN; e += 2) {
           const uint64_t y2 = f2fma(f2pack(x[e], x[e + 1]), c2, nm2);
           float p0, p1;
-          if (((e >> 1) & 7) < kFmaPairs) {
+          if (((e >> 1) & 7) < kFmaPairs<INT8>) {
             exp2_fma2(y2, p0, p1);
           } else {
             float y0, y1;
@@ -825,11 +836,11 @@ PageMaps page_maps(const PagedPool& pool, int d, bool int8, int rows) {
   return m;
 }
 
-template <int D, bool INT8>
-static tm_status launch_tile(const SharedArgs& a, bool prefix, bool overlap, DevErr err, cudaStream_t stream) {
+template <int D, bool INT8, bool prefix>
+static tm_status launch_tile(const SharedArgs& a, bool overlap, DevErr err, cudaStream_t stream) {
   using C = CfgT<D, INT8>;
   static std::atomic<uint64_t> prepared{0};
-  tm_status st = prepare_smem(tile_kernel<D, INT8>, C::SMEM, prepared);
+  tm_status st = prepare_smem(tile_kernel<D, INT8, prefix>, C::SMEM, prepared);
   if (st != TM_OK) return st;
   const SharedPlan& p = a.plan;
   TileMaps m{};
@@ -842,16 +853,28 @@ static tm_status launch_tile(const SharedArgs& a, bool prefix, bool overlap, Dev
     m.q_tma = encode_tiled_map(&m.q, a.q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, qdims, qstrides, qbox,
                                CU_TENSOR_MAP_SWIZZLE_128B);
   }
-  const int64_t items = prefix ? p.pre_ctas : static_cast<int64_t>(p.own_splits) * a.batch * p.own_rows * a.pool.H;
-  return launch_kernel(tile_kernel<D, INT8>, items, C::THREADS, C::SMEM, overlap, stream, a, m, prefix ? 1 : 0, err);
+  int64_t items = p.pre_ctas;
+  if (!prefix) {
+    // one CTA for each SM, which goes through several items: a CTA's start (setup, first copies, cold instructions) is
+    // as long as five key tiles
+    items = static_cast<int64_t>(p.own_splits) * a.batch * p.own_rows * a.pool.H;
+    if (items > 0x7fffffff) return TM_ERR_UNSUPPORTED;
+    if (items > kSmsB200) items = kSmsB200;
+  }
+  return launch_kernel(tile_kernel<D, INT8, prefix>, items, C::THREADS, C::SMEM, overlap, stream, a, m, err);
+}
+
+template <int D, bool INT8>
+static tm_status launch_tile_of(const SharedArgs& a, bool prefix, bool overlap, DevErr err, cudaStream_t stream) {
+  return prefix ? launch_tile<D, INT8, true>(a, overlap, err, stream) : launch_tile<D, INT8, false>(a, overlap, err, stream);
 }
 
 tm_status shared_tile(const SharedArgs& a, int d, bool int8, bool prefix, bool overlap, DevErr err,
                       cudaStream_t stream) {
-  if (d == 128) return int8 ? launch_tile<128, true>(a, prefix, overlap, err, stream)
-                            : launch_tile<128, false>(a, prefix, overlap, err, stream);
-  return int8 ? launch_tile<64, true>(a, prefix, overlap, err, stream)
-              : launch_tile<64, false>(a, prefix, overlap, err, stream);
+  if (d == 128) return int8 ? launch_tile_of<128, true>(a, prefix, overlap, err, stream)
+                            : launch_tile_of<128, false>(a, prefix, overlap, err, stream);
+  return int8 ? launch_tile_of<64, true>(a, prefix, overlap, err, stream)
+              : launch_tile_of<64, false>(a, prefix, overlap, err, stream);
 }
 
 }  // namespace tmk

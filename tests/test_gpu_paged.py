@@ -296,8 +296,19 @@ def test_attention(d, page, hq, hkv, int8, order, lens, new, prefix):
 @pytest.mark.parametrize("d,page,hq,hkv,int8,order", CACHES)
 @pytest.mark.parametrize("prefix", [2300, 2304])
 def test_attention_on_tiles(d, page, hq, hkv, int8, order, prefix):
-    """Rows and keys enough for the tile kernel, on both sides of the prefix's end; rows behind the last sequence."""
+    """Enough rows and keys for the tile kernel: chunks of prompts, with the prefix folded in, and short rows of many
+    sequences, with a pass of its own for the prefix; rows behind the last sequence."""
     attend(43, [301, 100, 4, 0], [300, 100, 1, 0], prefix, d, page, hq, hkv, int8, order, tail=3)
+    attend(47, [20 + i for i in range(70)], [1 + i % 11 for i in range(70)], prefix, d, page, hq, hkv, int8, order, tail=3)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("lens,new", [([0, 3, 200], [90, 3, 70]), ([2500, 40], [100, 40]), ([900], [700])])
+@pytest.mark.parametrize("prefix", [1, 128, 200, 777])
+def test_attention_with_the_prefix_folded_in(lens, new, prefix, int8):
+    """Own tokens behind the prefix's whole tiles: rows that see the prefix only, splits that end in either part."""
+    attend(48, lens, new, prefix, 128, 16, 4, 2, int8)
+    attend(49, lens, new, prefix, 64, 256, 4, 1, int8, "head", causal=False)
 
 
 @pytest.mark.parametrize("hq,hkv", [(28, 4), (6, 2), (8, 2)])
@@ -345,7 +356,7 @@ def test_attention_flat_and_peaked(scale):
 @pytest.mark.parametrize("prefix", [150, 2500])        # on the split-key kernel, on the tile kernel
 def test_attention_ignores_what_no_row_sees(prefix):
     """NaN and infinities in unused slots, unused pages and (as keys) at causally hidden positions change nothing."""
-    lens, new, prefix, page = [70, 21, 140], [1, 1, 130], prefix, 64
+    lens, new, page = [70, 21, 140] + [9] * 40, [1, 1, 130] + [3] * 40, 64
     g = gen(27)
     table, shared, total = make_table(27, lens, page, extra=prefix)
     q = randn(g, sum(new), 8, 128)
@@ -499,5 +510,5 @@ def test_offsets_past_32_bits():
 
 @pytest.mark.parametrize("d,int8", [(128, False), (64, True), (128, True), (64, False)])
 def test_attention_pieces_of_row_blocks(d, int8):
-    """More key tiles of the prefix than SMs; ragged own rows of several tiles."""
-    attend(41, [260, 90, 2], [110, 90, 1], 2500, d, 32, 16, 4, int8)
+    """More key tiles of the prefix than SMs."""
+    attend(41, [40 + i for i in range(60)], [1 + i % 5 for i in range(60)], 2500, d, 32, 16, 4, int8)
