@@ -722,7 +722,7 @@ class PagedKV:
                     raise ValueError("k_scales, v_scales: fp16 [num_pages, page_size, Hkv] of one layout expected")
             st = k_scales.stride()
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         self.num_pages, self.page_size, self.H, self.d = k.shape
         if self.d not in (64, 128) or self.page_size not in (16, 32, 64, 128, 256):
             raise ValueError("page_size in {16, 32, 64, 128, 256} and d in {64, 128} expected")
@@ -735,30 +735,35 @@ class PagedKV:
 # The current stream's handle without a Stream object around it (0.1 us instead of 3.4).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
-_HALF = torch.float16
+_HALF, _INT32 = torch.float16, torch.int32
 
 
-def _call(dev, name, *args):
-    """A library entry on the current stream of dev, whichever device is current."""
+def _call(index, name, *args):
+    """A library entry on the current stream of CUDA device `index`, whichever device is current."""
     fn = getattr(_LIB or _lib(), name)
-    index = dev.index
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            st = fn(*args, _raw_stream(index))
-    else:
+    if index == torch.cuda.current_device():
         st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
     if st != TM_OK:
         raise TmError(st, name)
 
 
-def _thd(x, name, dev, T=None, H=None, d=None):
-    """tm_tensor of an fp16 [T, H, d] operand on dev."""
+def _on(x, name, index):
+    """x lies on CUDA device `index` (-1: x is what the call goes by, and is not on one)."""
+    if x.get_device() != index or index < 0:
+        _cuda(x, name)
+        raise ValueError(f"{name}: on {x.device}, the call is on cuda:{index}")
+
+
+def _thd(x, name, index, T=None, H=None, d=None):
+    """tm_tensor of an fp16 [T, H, d] operand on CUDA device `index`."""
     shape = x.shape
     if x.dtype is not _HALF or len(shape) != 3:
         raise ValueError(f"{name}: fp16 [T, H, d] expected")
-    if x.device != dev or dev.type != "cuda":
-        _cuda(x, name)
-        raise ValueError(f"{name}: on {x.device}, the call is on {dev}")
+    if x.get_device() != index or index < 0:
+        _on(x, name, index)
     a, b, c = shape
     st, sh, sd = x.stride()
     if sd != 1 and c != 1:
@@ -768,45 +773,54 @@ def _thd(x, name, dev, T=None, H=None, d=None):
     return TmTensor(x.data_ptr(), a, b, c, st, sh)
 
 
-def _int32(t, name, dev, n=None):
+def _int32(t, name, index, n=None):
     """Device address of a contiguous int32 vector of at least n elements (None passes)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"{name}: contiguous int32 vector on {dev} expected")
-    if n is not None and t.shape[0] < n:
-        raise ValueError(f"{name}: at least {n} elements expected, got {t.shape[0]}")
+    shape = t.shape
+    if t.dtype is not _INT32 or len(shape) != 1 or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous int32 vector expected")
+    if t.get_device() != index:
+        _on(t, name, index)
+    if n is not None and shape[0] < n:
+        raise ValueError(f"{name}: at least {n} elements expected, got {shape[0]}")
     return t.data_ptr()
 
 
-def _weight(w, name, dev, d):
+def _weight(w, name, index, d):
     if w is None:
         return None
-    if w.dtype != torch.float16 or w.shape != (d,) or not w.is_contiguous() or w.device != dev:
-        raise ValueError(f"{name}: contiguous fp16 [{d}] on {dev} expected")
+    if w.dtype is not _HALF or w.shape != (d,) or not w.is_contiguous():
+        raise ValueError(f"{name}: contiguous fp16 [{d}] expected")
+    if w.get_device() != index:
+        _on(w, name, index)
     return w.data_ptr()
 
 
 def _table(block_table, kv, batch=None):
-    """(address, row stride, columns, rows) of an int32 [batch, columns] block table."""
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.device != kv.device:
-        raise ValueError(f"block_table: int32 [batch, columns] on {kv.device} expected")
-    n, cols = block_table.shape
-    if n < 1 or cols < 1 or (cols > 1 and block_table.stride(1) != 1):
+    """(address, row stride, columns) of an int32 [batch, columns] block table."""
+    shape = block_table.shape
+    if block_table.dtype is not _INT32 or len(shape) != 2:
+        raise ValueError("block_table: int32 [batch, columns] expected")
+    if block_table.get_device() != kv.index:
+        _on(block_table, "block_table", kv.index)
+    n, cols = shape
+    stride, one = block_table.stride()
+    if n < 1 or cols < 1 or (cols > 1 and one != 1):
         raise ValueError("block_table: at least one row and column, columns contiguous")
     if batch is not None and n < batch:
         raise ValueError(f"block_table: {batch} rows expected, got {n}")
-    return block_table.data_ptr(), block_table.stride(0), cols, n
+    return block_table.data_ptr(), stride, cols
 
 
 def _rope_call(name, q, k, out, rope, positions, pos_offset, *weights):
-    dev = q.device
+    dev = q.get_device()
     T, hq, d = q.shape
     if rope is not None and rope.d != d:
         raise ValueError(f"rope is for heads of {rope.d}, q has {d}")
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=dev),
-               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=dev))
+        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device))
     elif isinstance(out, torch.Tensor):
         out = (out, None)
     qo, ko = out
@@ -839,8 +853,8 @@ def qk_norm_rope(q, k=None, *, q_weight, k_weight=None, eps=1e-6, rope=None, pos
         raise ValueError("a weight for each of q and k expected")
     d = q.shape[2]
     return _rope_call("tm_qk_norm_rope", q, k, out, rope, positions, pos_offset,
-                      _weight(q_weight, "q_weight", q.device, d),
-                      _weight(k_weight if k is not None else None, "k_weight", q.device, d), float(eps))
+                      _weight(q_weight, "q_weight", q.get_device(), d),
+                      _weight(k_weight if k is not None else None, "k_weight", q.get_device(), d), float(eps))
 
 
 def block_table_check(block_table, kv_lens, num_pages, page_size):
@@ -869,10 +883,10 @@ def kv_append(k, v, kv, block_table, kv_lens, *, cu_seqlens=None, rope=None, pos
     (int32 [batch + 1]) or T / batch for each sequence.  pos_offset: length of
     a shared prefix.  Returns q_out (a new tensor if not given), or None
     without q."""
-    dev = kv.device
+    dev = kv.index
     T = k.shape[0]
     batch = kv_lens.shape[0]
-    ptr, stride, cols, _ = _table(block_table, kv, batch)
+    ptr, stride, cols = _table(block_table, kv, batch)
     if cu_seqlens is None and T % max(batch, 1):
         raise ValueError(f"{T} rows for {batch} sequences: cu_seqlens expected")
     if rope is not None and rope.d != kv.d:
@@ -898,11 +912,11 @@ def kv_gather(kv, block_table, cu_seqlens_k, *, out):
     [batch + 1]) sequence b's tokens in order: the keys and values of attn_fwd
     with cu_seqlens_k.  Returns out."""
     k, v = out
-    dev = kv.device
+    dev = kv.index
     batch = cu_seqlens_k.shape[0] - 1
     if batch < 1:
         raise ValueError("cu_seqlens_k: int32 [batch + 1] expected")
-    ptr, stride, cols, _ = _table(block_table, kv, batch)
+    ptr, stride, cols = _table(block_table, kv, batch)
     kd, vd = _thd(k, "k", dev, None, kv.H, kv.d), _thd(v, "v", dev, k.shape[0], kv.H, kv.d)
     _call(dev, "tm_kv_gather", kv.struct, ptr, stride, cols, _int32(cu_seqlens_k, "cu_seqlens_k", dev), batch,
           kd, vd)
@@ -931,12 +945,12 @@ def attn_shared_prefix(q, kv, block_table, kv_lens, *, prefix_pages=None, prefix
     kv_lens grow.  workspace: uint8, shared_prefix_workspace_bytes(...), one
     for each call that may run at the same time; allocated here when None.
     Returns out (a new tensor if not given)."""
-    dev = kv.device
+    dev = kv.index
     T, Hq = q.shape[0], q.shape[1]
     batch = kv_lens.shape[0]
     if batch < 1:
         raise ValueError("kv_lens: int32 [batch] expected")
-    ptr, stride, cols, _ = _table(block_table, kv, batch)
+    ptr, stride, cols = _table(block_table, kv, batch)
     if max_kv_len is None:
         max_kv_len = cols * kv.page_size
     if cu_seqlens is None:
@@ -952,9 +966,9 @@ def attn_shared_prefix(q, kv, block_table, kv_lens, *, prefix_pages=None, prefix
     if workspace is None:
         workspace = torch.empty(shared_prefix_workspace_bytes(kv, batch, T, Hq, max_seqlen=max_seqlen,
                                                               prefix_len=prefix_len, max_kv_len=max_kv_len),
-                                dtype=torch.uint8, device=dev)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError(f"workspace: contiguous uint8 on {dev} expected")
+                                dtype=torch.uint8, device=kv.device)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError(f"workspace: contiguous uint8 on {kv.device} expected")
     qd, od = _thd(q, "q", dev, T, Hq, kv.d), _thd(out, "out", dev, T, Hq, kv.d)
     _call(dev, "tm_attn_shared_prefix", qd, kv.struct, od, ptr, stride, cols,
           _int32(kv_lens, "kv_lens", dev), _int32(cu_seqlens, "cu_seqlens", dev, batch + 1), batch, int(max_seqlen),
