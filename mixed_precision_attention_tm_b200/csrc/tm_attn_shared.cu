@@ -286,16 +286,16 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
   auto entry_at = [&](int i) -> int32_t { return i < steps ? raw_entry(first + i * (kWarps * kStep)) : -1; };
   uint32_t by_tma = 0;      // bit s: stage s is filled by TMA
   struct Scales {
-    float k, v;
+    __half k, v;      // as loaded: a conversion would wait for the load
   };
   // INT8: a step's scales, as issue() loaded them, into its stage
   auto keep_scales = [&](int st, const Scales& x) {
     if (!INT8 || lane >= kStep) return;
     float* sc = scales + st * 3 * kStep + lane;
-    const float f = x.v == 0.f ? 5.9604645e-8f : x.v;   // a zero scale (codes all 0) counts in the row sum alone
-    sc[0] = x.k * a.scale_log2;
-    sc[kStep] = log2f(f);
-    sc[2 * kStep] = 1.0f / f;
+    const float v = __half2float(x.v), f = v == 0.f ? 5.9604645e-8f : v;   // a zero scale (codes all 0) counts in the row sum alone
+    sc[0] = __half2float(x.k) * a.scale_log2;
+    sc[kStep] = __log2f(f);             // within 2^-21: exact to the weights' 2^-18
+    sc[2 * kStep] = __frcp_rn(f);
   };
   // copies of step i into stage st
   auto issue = [&](int i, int st, int32_t page, Scales& sc) {
@@ -306,8 +306,11 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
       const int valid = ok ? min(k1 - key, kStep) : 0;
       if (INT8) {
         const int64_t so = page * a.pool.sstride_page + (s + lane) * a.pool.sstride_t + kvh * a.pool.sstride_h;
-        sc.k = lane < valid ? __half2float(a.pool.ks[so]) : 0.f;
-        sc.v = lane < valid ? __half2float(a.pool.vs[so]) : 0.f;
+        sc.k = sc.v = __float2half(0.f);
+        if (lane < valid) {
+          sc.k = a.pool.ks[so];
+          sc.v = a.pool.vs[so];
+        }
       }
       const uint32_t dst = ring_s + st * 2 * S::BYTES;
       if (maps.ok && valid == kStep) {
