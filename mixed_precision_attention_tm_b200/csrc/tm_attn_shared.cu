@@ -285,6 +285,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
   // page of step i as the table has it; -1 where nothing is to be read
   auto entry_at = [&](int i) -> int32_t { return i < steps ? raw_entry(first + i * (kWarps * kStep)) : -1; };
   uint32_t by_tma = 0;      // bit s: stage s is filled by TMA
+  const uint64_t policy = keys_policy(prefix ? p.pre_rows : p.own_rows);
   struct Scales {
     __half k, v;      // as loaded: a conversion would wait for the load
   };
@@ -321,8 +322,8 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
           const int32_t c1 = maps.heads_inner ? kvh : s, c2 = maps.heads_inner ? s : kvh;
 #pragma unroll
           for (int hh = 0; hh < (INT8 ? 1 : D / 64); ++hh) {
-            tma_load_4d(dst + hh * kStep * 128, &maps.k, bar, hh * 64, c1, c2, page);
-            tma_load_4d(dst + S::BYTES + hh * kStep * 128, &maps.v, bar, hh * 64, c1, c2, page);
+            tma_load_4d(dst + hh * kStep * 128, &maps.k, bar, hh * 64, c1, c2, page, policy);
+            tma_load_4d(dst + S::BYTES + hh * kStep * 128, &maps.v, bar, hh * 64, c1, c2, page, policy);
           }
         }
         __syncwarp();

@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
     const int boxes = 128 >> box_shift;
     const int LANDED = INT8 ? T_CODES : T_FULL;
     constexpr uint32_t DST = INT8 ? C::SLOT / 2 : 0;
+    const uint64_t policy = keys_policy(prefix ? p.pre_rows : p.fold > 0 ? 2 : p.own_rows);
     // a whole tile: lane i copies box i, whose page it holds
     auto copy_boxes = [&](const CUtensorMap* map, uint32_t slot, int32_t page, int key) {
       const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT + DST;
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
 #pragma unroll
         for (int hh = 0; hh < (INT8 ? 1 : D / 64); ++hh)
           tma_load_4d(tile + hh * C::HALF + (lane << box_shift) * (INT8 ? D : 128), map, bar(LANDED + slot), hh * 64,
-                      c1, c2, page);
+                      c1, c2, page, policy);
       }
       __syncwarp();
     };
