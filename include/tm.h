@@ -545,8 +545,8 @@ tm_status tm_qk_norm_rope(const tm_tensor* q, const tm_tensor* k, tm_tensor* q_o
 
 /* A pool of K/V pages.  Element c of head h of slot s of page p is at
  * k[p * stride_page + s * stride_t + h * stride_h + c], v alike: fp16, or INT8
- * codes when k_scales / v_scales are given (fp16, one per slot and head, at
- * p * scale_stride_page + s * scale_stride_t + h * scale_stride_h; a value is
+ * codes when k_scales / v_scales are given (fp16, >= 0, one per slot and head,
+ * at p * scale_stride_page + s * scale_stride_t + h * scale_stride_h; a value is
  * code * scale).  page_size in {16, 32, 64, 128, 256}; d in {64, 128}; k and v
  * 16-byte aligned, strides multiples of 16 bytes.  Pages of different tokens
  * must not overlap. */
@@ -612,10 +612,12 @@ tm_status tm_kv_gather(const tm_paged_kv* cache, const int32_t* table, int64_t t
  * by the whole batch) and own position j of its sequence iff j < kv_lens[b]
  * and (not causal or j <= i + kv_lens[b] - n_b).  One softmax runs over both:
  *   out = fp16( sum_j softmax_j(q . k_j / sqrt(d)) v_j )
- * fp32 scores, statistics and sums; P rounded to fp16 for the P.V product.  A
+ * fp32 scores, statistics and sums; P rounded to fp16 for the P.V product, the
+ * one rounding besides the result's (INT8 scales are applied in fp32).  A
  * row that sees nothing is 0; rows behind the last sequence are left as they
  * were.  Values at visible and causally hidden positions below kv_lens[b] must
  * be finite; the rest of a page is never used.
+ *   q, out: fp16 [T, Hq, d], Hq a multiple of the cache's H; out may be q.
  *   prefix_len = 0: plain paged attention (prefix_pages may be NULL).
  *   max_seqlen: bound on n_b (ignored without cu_seqlens); max_kv_len: bound
  *   on kv_lens[b], at most table_cols * page_size, sizes the launch; a longer

@@ -5,8 +5,8 @@
 // row r of a sequence (or of the whole batch, for the prefix) is token r / g,
 // query head kv_head * g + r % g, g = Hq / Hkv, so that every byte of K and V
 // is used for all rows that see it.  Keys are cut into ranges ("splits"); a
-// split's result for a row is (O, m, l): the running maximum m of its scores
-// in powers of two, l = sum 2^(s - m + kPOffset) and O = the same sum of
+// split's result for a row is (O, m, l): a reference m of its scores in powers
+// of two (a maximum of some time), l = sum 2^(s - m + kPOffset) and O = the same sum of
 // weighted values, fp32.  One slot of the workspace holds one split's results
 // of all rows, prefix splits first; results join as
 //   out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,  M = max m_i.
@@ -21,10 +21,11 @@ namespace tmk {
 
 constexpr int kSmsB200 = 148;
 
-// P is rounded to fp16 for the P.V product.  Its largest value is 2^kPOffset
-// instead of 1, which keeps weights down to 2^-20 of the largest normal fp16
-// numbers, and even with an INT8 cache's V scale (at most 65504 / 127 = 516 for
-// values fp16 holds) multiplied in, below fp16's 65504.
+// P is rounded to fp16 for the P.V product.  A weight is 2^kPOffset, not 1,
+// where the score equals the row's reference, so that weights down to 2^-20 of
+// that stay normal fp16 numbers; above the reference fp16 leaves 2^9 (2^8 where
+// a part of INT8 V's scale is multiplied in), by which scores may pass it before
+// it is raised.
 constexpr float kPOffset = 6.0f;
 
 // Which kernel takes the prefix, and which the own tokens.  The split-key
@@ -59,7 +60,7 @@ struct SharedPlan {
   int own_splits, pre_splits; // most results of a row
   int own_chunk;              // keys per split
   int fold;                   // key tiles of the prefix that the own tokens' row blocks go through first (no prefix results)
-  int pre_chunk;              // the same; on the tile kernel: key tiles per CTA
+  int pre_chunk;              // the same of the prefix; on the tile kernel: key tiles per CTA
   int pre_tiles, pre_ctas;    // tile kernel: key tiles of the prefix, CTAs
   int pre_pieces;             // tile kernel: pieces of a row block, 0: pieces of the whole line
   int slots;                  // own_splits + pre_splits
@@ -68,7 +69,7 @@ struct SharedPlan {
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, int32_t batch, int64_t max_seqlen,
+SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, bool int8, int32_t batch, int64_t max_seqlen,
                        int64_t prefix_len, int64_t max_kv_len);
 
 struct SharedArgs {

@@ -512,3 +512,42 @@ def test_offsets_past_32_bits():
 def test_attention_pieces_of_row_blocks(d, int8):
     """More key tiles of the prefix than SMs."""
     attend(41, [40 + i for i in range(60)], [1 + i % 5 for i in range(60)], 2500, d, 32, 16, 4, int8)
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [90, 2, 130]])
+@pytest.mark.parametrize("prefix", [0, 100])
+def test_in_place_queries(new, prefix):
+    """Queries rotated in place by the append, then the result in their place."""
+    g = gen(50)
+    lens = [150, 40, 140]
+    table, shared, total = make_table(50, lens, 32, extra=prefix)
+    kv = make_pool(g, total, 32, 2, 128, False)
+    T = sum(new)
+    q, k, v = randn(g, T, 8, 128), randn(g, T, 2, 128), randn(g, T, 2, 128)
+    args = dict(cu_seqlens=offsets(new))
+    r = ops.Rope(128)
+    want_q = ops.kv_append(k, v, kv, table, i32(lens), rope=r, pos_offset=prefix, q=q, **args)
+    assert ops.kv_append(k, v, kv, table, i32(lens), rope=r, pos_offset=prefix, q=q, q_out=q, **args) is q
+    args.update(max_seqlen=max(new), prefix_pages=shared, prefix_len=prefix)
+    want = ops.attn_shared_prefix(want_q, kv, table, i32(lens), **args)
+    ops.attn_shared_prefix(q, kv, table, i32(lens), out=q, **args)
+    ok()
+    assert torch.equal(q, want)
+
+
+def test_calls_on_another_stream():
+    """A call on a side stream, ordered by events only."""
+    g = gen(51)
+    table, shared, total = make_table(51, [70, 33], 16, extra=300)
+    kv = make_pool(g, total, 16, 2, 64, True)
+    q = randn(g, 2, 8, 64)
+    args = dict(prefix_pages=shared, prefix_len=300)
+    lens = i32([70, 33])
+    want = ops.attn_shared_prefix(q, kv, table, lens, **args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = [ops.attn_shared_prefix(q, kv, table, lens, **args) for _ in range(20)]
+    torch.cuda.current_stream().wait_stream(side)
+    ok()
+    assert all(torch.equal(x, want) for x in got)
