@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32, 6) token_kernel(const __grid
       const int32_t s = __ldg(a.cu + b);
       n = __ldg(a.cu + b + 1) - s;
       i = t - s;
+      if (i < 0) return;                   // before the first
     } else {
       b = static_cast<int>(t / a.per_seq);
       n = a.per_seq;
