@@ -25,8 +25,13 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, bool int8,
     pre_units = 0;
   }
   p.pre_tile = prefix_on_tiles(ceil_div(pre_packed, 16) * Hkv, ceil_div(pre_packed, 256) * Hkv, pre_units);
-  const int64_t own_rows = ceil_div(own_packed, p.own_tile ? 256 : 16);
-  const int64_t pre_rows = ceil_div(pre_packed, p.pre_tile ? 256 : 16);
+  // blocks of eight rows where sequences have no more, and a prefix in such blocks costs little next to them
+  p.narrow = !p.own_tile && own_packed <= split_block(true) &&
+             (p.pre_tile || pre_packed <= split_block(true) ||
+              4 * ceil_div(pre_packed, split_block(true)) * pre_units <= batch * own_units);
+  const int block = split_block(p.narrow);
+  const int64_t own_rows = ceil_div(own_packed, p.own_tile ? 256 : block);
+  const int64_t pre_rows = ceil_div(pre_packed, p.pre_tile ? 256 : block);
   p.own_rows = static_cast<int>(own_rows);
   p.pre_rows = static_cast<int>(pre_rows);
   // Split kernel: the pieces that end soonest, as waves of CTAs, each its key tiles and a start and end worth two
@@ -35,7 +40,7 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, bool int8,
   // Five CTAs per SM whatever the lengths took 13.7 us instead of 10.4 (8 tokens behind 2000 positions) and
   // 16.4 instead of 12.7 (20 sequences of up to 200 tokens behind 1000).
   const int64_t pre_blocks = p.pre_tile ? 0 : pre_rows * Hkv, own_blocks = p.own_tile ? 0 : batch * own_rows * Hkv;
-  const int64_t resident = (d == 64 ? 4 : int8 ? 3 : 2) * kSmsB200;
+  const int64_t resident = split_resident(d, int8, p.narrow) * kSmsB200;
   int64_t chunk = 1, best = 0;
   // With many own key tiles the lengths alone fill the last waves, and what counts is that the pieces are long: five
   // CTAs per SM (32 sequences of up to 2000 tokens, INT8: 32.0 us, by waves 37.9).
@@ -142,6 +147,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// An 8 x 8 matrix of fp16, two columns of row lane / 4 in each lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
@@ -197,11 +208,13 @@ struct SplitSmem {
 // follow the fragments: the order of d within the QK^T sum is free, so a
 // lane's 16 consecutive codes serve four MMAs; the order of output columns is
 // free too, so a lane's n index stands for d / 8 consecutive dimensions.
-template <int D, bool INT8>
+template <int D, bool INT8, bool NARROW>
 __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& maps, DevErr err) {
   using S = Stage<D, INT8>;
   using L_ = SplitSmem<D, INT8>;
-  constexpr int NT = D / 8, KS = D / 16;
+  constexpr int KS = D / 16;
+  constexpr int NT = NARROW ? D / 16 : D / 8;      // tiles of O
+  constexpr int BR = split_block(NARROW);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -219,7 +232,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
   int hidden = 0;         // own, causal: token i of the sequence sees keys below hidden + i
   if (prefix) {
     slot = item / p.pre_rows;
-    row0 = (item - slot * p.pre_rows) * 16;
+    row0 = (item - slot * p.pre_rows) * BR;
     nrows = static_cast<int>(a.T) * g;
     k0 = slot * p.pre_chunk;
     k1 = min(k0 + p.pre_chunk, static_cast<int>(a.prefix_len));
@@ -229,7 +242,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
     const int split = item / per;
     item -= split * per;
     b = item / p.own_rows;
-    row0 = (item - b * p.own_rows) * 16;
+    row0 = (item - b * p.own_rows) * BR;
     slot = p.pre_splits + split;
     k0 = split * p.own_chunk;
   }
@@ -246,7 +259,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
   if (!prefix) {
     int64_t start64, n64;
     seq_rows(a, b, start64, n64);
-    const bool outside = start64 < 0 || n64 < 0 || start64 + n64 > a.T || n64 * g > static_cast<int64_t>(p.own_rows) * 16;
+    const bool outside = start64 < 0 || n64 < 0 || start64 + n64 > a.T || n64 * g > static_cast<int64_t>(p.own_rows) * BR;
     if (outside && threadIdx.x == 0) dev_error(err, TM_DEVERR_SEQLEN);   // offsets that the launch was not sized for
     const int n = static_cast<int>(n64);
     if (outside || row0 >= n * g) return;
@@ -260,9 +273,9 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
     lk = max(lk, 0);
     hidden = lk - n + 1;
     k1 = min(k0 + p.own_chunk, lk);
-    if (a.causal) k1 = min(k1, hidden + (min(row0 + 16, nrows) - 1) / g);   // keys that the block's last row sees
+    if (a.causal) k1 = min(k1, hidden + (min(row0 + BR, nrows) - 1) / g);   // keys that the block's last row sees
   }
-  const int rows = min(nrows - row0, 16);
+  const int rows = min(nrows - row0, BR);
   const int64_t total = a.T * Hq;
   const bool direct = p.slots == 1;
 
@@ -313,7 +326,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
     float* sc = scales + st * 3 * kStep + lane;
     const float v = __half2float(x.v), f = v == 0.f ? 5.9604645e-8f : v;   // a zero scale (codes all 0) counts in the row sum alone
     sc[0] = __half2float(x.k) * a.scale_log2;
-    sc[kStep] = __log2f(f);             // within 2^-21: exact to the weights' 2^-18
+    sc[kStep] = __log2f(f);             // within 2^-18 (two units in the last place of up to 24): a weight's relative error
     sc[2 * kStep] = __frcp_rn(f);
   };
   // copies of step i into stage st
@@ -366,15 +379,21 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
   issue(1, 1, page1, sc_b);
   page = page2;
 
-  // ---- this lane's rows r8 and r8 + 8: limits and Q fragments, while the first copies are under way
+  // ---- this lane's rows: limits and Q fragments, while the first copies are under way
+  // In scores, weights and O a lane holds rows r8 and r8 + 8 (NARROW: 2 quad and 2 quad + 1).
+  auto row_of = [&](int h) { return NARROW ? 2 * quad + h : r8 + 8 * h; };
   int lim[2];
-  uint32_t qf[KS][4];
+  uint32_t qf[KS][NARROW ? 2 : 4];      // NARROW: the B operand, row r8
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
+    lim[i] = k1;
+    if (!prefix && a.causal && row_of(i) < rows) lim[i] = min(k1, hidden + (row0 + row_of(i)) / g);
+  }
+  constexpr int QH = NARROW ? 1 : 2;
+#pragma unroll
+  for (int i = 0; i < QH; ++i) {
     const int r = r8 + 8 * i;
     const bool real = r < rows;
-    lim[i] = k1;
-    if (!prefix && a.causal && real) lim[i] = min(k1, hidden + (row0 + r) / g);
     const __half* q = real ? a.q + token_of(r) * a.q_t + head_of(r) * a.q_h : a.q;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
@@ -383,10 +402,10 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
         const int at = (s >> 2) * 64 + quad * 16 + (s & 3) * 4;
         const uint2 v = real ? *reinterpret_cast<const uint2*>(q + at) : make_uint2(0, 0);
         qf[s][i] = v.x;
-        qf[s][2 + i] = v.y;
+        qf[s][QH + i] = v.y;
       } else {
         qf[s][i] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * quad) : 0u;
-        qf[s][2 + i] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 8 + 2 * quad) : 0u;
+        qf[s][QH + i] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 8 + 2 * quad) : 0u;
       }
     }
   }
@@ -415,83 +434,122 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
     page = entry_at(i + 3);
     const uint32_t ks_s = ring_s + st * 2 * S::BYTES;
     const uint32_t vs_s = ks_s + S::BYTES;
-    const float* sc = scales + st * 3 * kStep + 2 * quad;
+    const int sc_st = st;
     const int key0 = first + i * (kWarps * kStep);
     st = st == kStages - 1 ? 0 : st + 1;
 
-    // even and odd halves of d in sums of their own: half the chain of dependent MMAs
-    float s[2][4], s2[2][4];
+    // Scores: x[j][2 h + e] is key 8 j + 2 quad + e against row r8 + 8 h; NARROW: x[j][h] key 8 j + r8 against row 2 quad + h
+    constexpr int XE = NARROW ? 2 : 4;
+    float x[2][XE], iv[2][2];
+    const float* sc = scales + sc_st * 3 * kStep + (NARROW ? r8 : 2 * quad);
+    if constexpr (NARROW) {
+      // K is the A operand; four sums, so that two dependent MMAs are the longest chain at d = 128
+      float s[4][4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+      if (!INT8) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[j][e] = s2[j][e] = 0.f;
-    }
-    if (!INT8) {
-#pragma unroll
-      for (int ks = 0; ks < KS; ks += 2) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t bfr[4];
-          ldsm4(ks_s + S::at(8 * j + (lane & 7), 2 * ks + (lane >> 3)), bfr);
-          mma16816(s[j], qf[ks], bfr[0], bfr[1]);
-          mma16816(s2[j], qf[ks + 1], bfr[2], bfr[3]);
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t afr[4];
+          ldsm4(ks_s + S::at(lane & 15, 2 * ks + (lane >> 4)), afr);
+          mma16816(s[ks & 3], afr, qf[ks][0], qf[ks][1]);
         }
+      } else {
+#pragma unroll
+        for (int c = 0; c < KS / 4; ++c) {
+          const uint4 v = lds128(ks_s + S::at(r8, 4 * c + quad)), u = lds128(ks_s + S::at(8 + r8, 4 * c + quad));
+          const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+          const uint32_t y[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t afr[4] = {codes2(w[e], 0x4140u), codes2(y[e], 0x4140u), codes2(w[e], 0x4342u),
+                                     codes2(y[e], 0x4342u)};
+            mma16816(s[e], afr, qf[4 * c + e][0], qf[4 * c + e][1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float kj = INT8 ? sc[8 * j] : a.scale_log2, vj = INT8 ? sc[kStep + 8 * j] : 0.f;
+        iv[j][0] = iv[j][1] = INT8 ? sc[2 * kStep + 8 * j] : 1.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          x[j][h] = ((s[0][2 * j + h] + s[1][2 * j + h]) + (s[2][2 * j + h] + s[3][2 * j + h])) * kj + vj;
       }
     } else {
+      // even and odd halves of d in sums of their own: half the chain of dependent MMAs
+      float s[2][4], s2[2][4];
 #pragma unroll
-      for (int c = 0; c < KS / 4; ++c) {
+      for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4 v = lds128(ks_s + S::at(8 * j + r8, 4 * c + quad));
-          const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+        for (int e = 0; e < 4; ++e) s[j][e] = s2[j][e] = 0.f;
+      }
+      if (!INT8) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mma16816(e & 1 ? s2[j] : s[j], qf[4 * c + e], codes2(w[e], 0x4140u), codes2(w[e], 0x4342u));
+        for (int ks = 0; ks < KS; ks += 2) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t bfr[4];
+            ldsm4(ks_s + S::at(8 * j + (lane & 7), 2 * ks + (lane >> 3)), bfr);
+            mma16816(s[j], qf[ks], bfr[0], bfr[1]);
+            mma16816(s2[j], qf[ks + 1], bfr[2], bfr[3]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < KS / 4; ++c) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 v = lds128(ks_s + S::at(8 * j + r8, 4 * c + quad));
+            const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mma16816(e & 1 ? s2[j] : s[j], qf[4 * c + e], codes2(w[e], 0x4140u), codes2(w[e], 0x4342u));
+          }
         }
       }
-    }
-
-    // scores in powers of two; hidden keys to -inf by selection, whatever they hold
-    float x[2][4], iv[2][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float k0s = a.scale_log2, k1s = a.scale_log2, v0 = 0.f, v1 = 0.f;
-      if (INT8) {
-        const float2 fk = *reinterpret_cast<const float2*>(sc + 8 * j);
-        const float2 fv = *reinterpret_cast<const float2*>(sc + kStep + 8 * j);
-        const float2 fi = *reinterpret_cast<const float2*>(sc + 2 * kStep + 8 * j);
-        k0s = fk.x;
-        k1s = fk.y;
-        v0 = fv.x;
-        v1 = fv.y;
-        iv[j][0] = fi.x;
-        iv[j][1] = fi.y;
+      for (int j = 0; j < 2; ++j) {
+        float k0s = a.scale_log2, k1s = a.scale_log2, v0 = 0.f, v1 = 0.f;
+        if (INT8) {
+          const float2 fk = *reinterpret_cast<const float2*>(sc + 8 * j);
+          const float2 fv = *reinterpret_cast<const float2*>(sc + kStep + 8 * j);
+          const float2 fi = *reinterpret_cast<const float2*>(sc + 2 * kStep + 8 * j);
+          k0s = fk.x;
+          k1s = fk.y;
+          v0 = fv.x;
+          v1 = fv.y;
+          iv[j][0] = fi.x;
+          iv[j][1] = fi.y;
+        }
+        x[j][0] = (s[j][0] + s2[j][0]) * k0s + v0;
+        x[j][1] = (s[j][1] + s2[j][1]) * k1s + v1;
+        x[j][2] = (s[j][2] + s2[j][2]) * k0s + v0;
+        x[j][3] = (s[j][3] + s2[j][3]) * k1s + v1;
       }
-      x[j][0] = (s[j][0] + s2[j][0]) * k0s + v0;
-      x[j][1] = (s[j][1] + s2[j][1]) * k1s + v1;
-      x[j][2] = (s[j][2] + s2[j][2]) * k0s + v0;
-      x[j][3] = (s[j][3] + s2[j][3]) * k1s + v1;
     }
+    // hidden keys to -inf by selection, whatever they hold
     if (key0 + kStep > open) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = key0 + 8 * j + 2 * quad + (e & 1);
-          if (key >= lim[e >> 1]) x[j][e] = -INFINITY;
+        for (int e = 0; e < XE; ++e) {
+          const int key = key0 + 8 * j + (NARROW ? r8 : 2 * quad + (e & 1));
+          if (key >= lim[NARROW ? e : e >> 1]) x[j][e] = -INFINITY;
         }
       }
     }
     // the references are raised (and O and l rescaled) only when a score exceeds one by 2^kLazy
     float mx[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) mx[h] = fmaxf(fmaxf(x[0][2 * h], x[0][2 * h + 1]), fmaxf(x[1][2 * h], x[1][2 * h + 1]));
+    for (int h = 0; h < 2; ++h)
+      mx[h] = NARROW ? fmaxf(x[0][h], x[1][h])
+                     : fmaxf(fmaxf(x[0][XE / 2 * h], x[0][XE / 2 * h + 1]), fmaxf(x[1][XE / 2 * h], x[1][XE / 2 * h + 1]));
     if (__any_sync(0xffffffffu, mx[0] > m[0] + kLazy || mx[1] > m[1] + kLazy)) {
       float scale[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        for (int w = NARROW ? 4 : 1; w < (NARROW ? 32 : 4); w *= 2) mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], w));
         const float mn = fmaxf(m[h], mx[h]);
         scale[h] = ex2_approx(m[h] - (mn == -INFINITY ? 0.f : mn));
         m[h] = mn;
@@ -499,10 +557,8 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        o[n][0] *= scale[0];
-        o[n][1] *= scale[0];
-        o[n][2] *= scale[1];
-        o[n][3] *= scale[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] *= scale[NARROW ? e & 1 : e >> 1];
       }
     }
 #pragma unroll
@@ -512,27 +568,46 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float pr = ex2_approx(x[j][2 * h + e] - use);
-          x[j][2 * h + e] = pr;
+        for (int e = 0; e < XE / 2; ++e) {
+          const float pr = ex2_approx(x[j][XE / 2 * h + e] - use);
+          x[j][XE / 2 * h + e] = pr;
           sum += INT8 ? pr * iv[j][e] : pr;
         }
       }
       l[h] += sum;
     }
-    const uint32_t pf[4] = {pack_half2(x[0][0], x[0][1]), pack_half2(x[0][2], x[0][3]), pack_half2(x[1][0], x[1][1]),
-                            pack_half2(x[1][2], x[1][3])};
+    // P as an operand: rows and keys as the scores have them; NARROW: keys 2 quad .. against row r8, so transposed
+    uint32_t pf[4];
+    if constexpr (NARROW) {
+      pf[0] = transpose8(pack_half2(x[0][0], x[0][1]));
+      pf[1] = transpose8(pack_half2(x[1][0], x[1][1]));
+    } else {
+      pf[0] = pack_half2(x[0][0], x[0][1]);
+      pf[1] = pack_half2(x[0][XE - 2], x[0][XE - 1]);
+      pf[2] = pack_half2(x[1][0], x[1][1]);
+      pf[3] = pack_half2(x[1][XE - 2], x[1][XE - 1]);
+    }
     if (!INT8) {
+      if constexpr (NARROW) {
+        // V^T is the A operand: dimensions 16 n + r8 and 8 more, keys 2 quad .. and 8 more
 #pragma unroll
-      for (int n = 0; n < NT; n += 2) {
-        uint32_t bfr[4];
-        ldsm4t(vs_s + S::at(((lane >> 3) & 1) * 8 + (lane & 7), n + (lane >> 4)), bfr);
-        mma16816(o[n], pf, bfr[0], bfr[1]);
-        mma16816(o[n + 1], pf, bfr[2], bfr[3]);
+        for (int n = 0; n < NT; ++n) {
+          uint32_t afr[4];
+          ldsm4t(vs_s + S::at((lane >> 4) * 8 + (lane & 7), 2 * n + ((lane >> 3) & 1)), afr);
+          mma16816(o[n], afr, pf[0], pf[1]);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          uint32_t bfr[4];
+          ldsm4t(vs_s + S::at(((lane >> 3) & 1) * 8 + (lane & 7), n + (lane >> 4)), bfr);
+          mma16816(o[n], pf, bfr[0], bfr[1]);
+          mma16816(o[n + 1], pf, bfr[2], bfr[3]);
+        }
       }
     } else {
-      // keys 2 quad, 2 quad + 1, 2 quad + 8, 2 quad + 9 of the 16; this lane's n index r8 stands for
-      // dimensions r8 * (D / 8) + n of n-tile n
+      // keys 2 quad, 2 quad + 1, 2 quad + 8, 2 quad + 9 of the 16; this lane's index r8 stands for dimensions
+      // r8 * (D / 8) + n: of n-tile n, or (NARROW) of rows r8 and r8 + 8 of tile n / 2 by turns
       uint32_t w[4][D / 32];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -555,8 +630,13 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
         for (int hlf = 0; hlf < 2; ++hlf) {
           const uint32_t lo = __byte_perm(w[0][q], w[1][q], hlf ? 0x7362u : 0x5140u);
           const uint32_t hi = __byte_perm(w[2][q], w[3][q], hlf ? 0x7362u : 0x5140u);
-          mma16816(o[4 * q + 2 * hlf], pf, codes2(lo, 0x4140u), codes2(hi, 0x4140u));
-          mma16816(o[4 * q + 2 * hlf + 1], pf, codes2(lo, 0x4342u), codes2(hi, 0x4342u));
+          const uint32_t v[4] = {codes2(lo, 0x4140u), codes2(lo, 0x4342u), codes2(hi, 0x4140u), codes2(hi, 0x4342u)};
+          if constexpr (NARROW) {
+            mma16816(o[2 * q + hlf], v, pf[0], pf[1]);
+          } else {
+            mma16816(o[4 * q + 2 * hlf], pf, v[0], v[2]);
+            mma16816(o[4 * q + 2 * hlf + 1], pf, v[1], v[3]);
+          }
         }
       }
     }
@@ -565,14 +645,14 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
   cp_wait<0>();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    for (int w = NARROW ? 4 : 1; w < (NARROW ? 32 : 4); w *= 2) l[h] += __shfl_xor_sync(0xffffffffu, l[h], w);
   }
 
   // ---- join the four warps, in fragment order: register e of n-tile n of lane
-  if (quad == 0) {
-    ml_s[warp * 16 + r8] = make_float2(m[0], l[0]);
-    ml_s[warp * 16 + r8 + 8] = make_float2(m[1], l[1]);
+  const bool writer = NARROW ? r8 == 0 : quad == 0;      // of its rows' m and l
+  if (writer) {
+    ml_s[warp * 16 + row_of(0)] = make_float2(m[0], l[0]);
+    ml_s[warp * 16 + row_of(1)] = make_float2(m[1], l[1]);
   }
   __syncwarp();
   static_assert(NT * 32 * 16 <= kStages * 2 * S::BYTES, "a warp's O fits its ring");
@@ -587,11 +667,11 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
     M[h] = -INFINITY;
     L[h] = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M[h] = fmaxf(M[h], ml_s[w * 16 + r8 + 8 * h].x);
+    for (int w = 0; w < kWarps; ++w) M[h] = fmaxf(M[h], ml_s[w * 16 + row_of(h)].x);
     const float use = M[h] == -INFINITY ? 0.f : M[h];
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float2 f = ml_s[w * 16 + r8 + 8 * h];
+      const float2 f = ml_s[w * 16 + row_of(h)];
       wgt[h][w] = ex2_approx(f.x - use);
       L[h] += wgt[h][w] * f.y;
     }
@@ -611,23 +691,45 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
       const float* src = reinterpret_cast<const float*>(smem + w * kStages * 2 * S::BYTES);
       const float4 f = *reinterpret_cast<const float4*>(src + ((warp * NW + n) * 32 + lane) * 4);
       acc[n][0] += wgt[0][w] * f.x;
-      acc[n][1] += wgt[0][w] * f.y;
-      acc[n][2] += wgt[1][w] * f.z;
+      acc[n][1] += wgt[NARROW ? 1 : 0][w] * f.y;
+      acc[n][2] += wgt[NARROW ? 0 : 1][w] * f.z;
       acc[n][3] += wgt[1][w] * f.w;
     }
   }
   const int64_t used = direct ? rows_in_use(a) : 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int r = r8 + 8 * h;
+    const int r = row_of(h);
     if (r >= rows) continue;
     const int64_t t = token_of(r);
     const int64_t idx = slot * total + t * Hq + head_of(r);
-    if (!direct && warp == 0 && quad == 0) a.ml[idx] = make_float2(M[h], L[h]);
+    if (!direct && warp == 0 && writer) a.ml[idx] = make_float2(M[h], L[h]);
     if (direct && t >= used) continue;
     __half* oh = direct ? a.out + t * a.o_t + head_of(r) * a.o_h : nullptr;
     float* of = direct ? nullptr : a.o + idx * D;
-    if (INT8) {
+    if (NARROW && INT8) {
+      // tiles warp * NW ..: 2 NW consecutive dimensions
+#pragma unroll
+      for (int n = 0; n < NW; ++n) {
+        const int at = r8 * (D / 8) + 2 * (warp * NW + n);
+        if (direct)
+          *reinterpret_cast<uint32_t*>(oh + at) = pack_half2(acc[n][h], acc[n][2 + h]);
+        else
+          *reinterpret_cast<float2*>(of + at) = make_float2(acc[n][h], acc[n][2 + h]);
+      }
+    } else if (NARROW) {
+#pragma unroll
+      for (int n = 0; n < NW; ++n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int at = (warp * NW + n) * 16 + 8 * e + r8;
+          if (direct)
+            oh[at] = __float2half_rn(acc[n][2 * e + h]);
+          else
+            of[at] = acc[n][2 * e + h];
+        }
+      }
+    } else if (INT8) {
       // n-tiles warp * NW ..: consecutive dimensions for each of the lane's two columns
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -635,9 +737,9 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
 #pragma unroll
         for (int n = 0; n < NW; n += 2) {
           if (direct)
-            *reinterpret_cast<uint32_t*>(oh + at + n) = pack_half2(acc[n][2 * h + e], acc[n + 1][2 * h + e]);
+            *reinterpret_cast<uint32_t*>(oh + at + n) = pack_half2(acc[n][2 * h + e], acc[n + 1 < NW ? n + 1 : n][2 * h + e]);
           else
-            *reinterpret_cast<float2*>(of + at + n) = make_float2(acc[n][2 * h + e], acc[n + 1][2 * h + e]);
+            *reinterpret_cast<float2*>(of + at + n) = make_float2(acc[n][2 * h + e], acc[n + 1 < NW ? n + 1 : n][2 * h + e]);
         }
       }
     } else {
@@ -653,11 +755,11 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
   }
 }
 
-template <int D, bool INT8>
-__global__ void __launch_bounds__(kWarps * 32)
+template <int D, bool INT8, bool NARROW>
+__global__ void __launch_bounds__(kWarps * 32, split_resident(D, INT8, NARROW))
     split_kernel(const __grid_constant__ SharedArgs a, const __grid_constant__ PageMaps maps, DevErr err) {
   pdl_launch_dependents();
-  split_rows<D, INT8>(a, maps, err);
+  split_rows<D, INT8, NARROW>(a, maps, err);
   pdl_wait();      // whoever waits for this kernel has waited for the one before it
 }
 
@@ -840,16 +942,16 @@ __global__ void __launch_bounds__(256, 4) join_kernel(const __grid_constant__ Sh
     *reinterpret_cast<uint32_t*>(dst) = pack_half2(acc[0] * inv, acc[1] * inv);
 }
 
-template <int D, bool INT8>
+template <int D, bool INT8, bool NARROW>
 tm_status launch_split(const SharedArgs& a, bool overlap, DevErr err, cudaStream_t stream) {
   constexpr int smem = SplitSmem<D, INT8>::BYTES;
   static std::atomic<uint64_t> prepared{0};
-  const tm_status st = prepare_smem(split_kernel<D, INT8>, smem, prepared);
+  const tm_status st = prepare_smem(split_kernel<D, INT8, NARROW>, smem, prepared);
   if (st != TM_OK) return st;
   const SharedPlan& p = a.plan;
   const int64_t items = ((p.pre_tile ? 0 : static_cast<int64_t>(p.pre_splits) * p.pre_rows) +
                          (p.own_tile ? 0 : static_cast<int64_t>(p.own_splits) * a.batch * p.own_rows)) * a.pool.H;
-  return launch_kernel(split_kernel<D, INT8>, items, kWarps * 32, smem, overlap, stream, a,
+  return launch_kernel(split_kernel<D, INT8, NARROW>, items, kWarps * 32, smem, overlap, stream, a,
                        page_maps(a.pool, D, INT8, kStep), err);
 }
 
@@ -868,8 +970,11 @@ tm_status launch(const SharedArgs& a, int d, bool int8, DevErr err, cudaStream_t
     after = true;
   }
   if (st == TM_OK && ((!p.pre_tile && p.pre_splits > 0) || (!p.own_tile && p.own_splits > 0))) {
-    st = d == 128 ? (int8 ? launch_split<128, true>(a, after, err, stream) : launch_split<128, false>(a, after, err, stream))
-                  : (int8 ? launch_split<64, true>(a, after, err, stream) : launch_split<64, false>(a, after, err, stream));
+    auto split = p.narrow ? (d == 128 ? (int8 ? launch_split<128, true, true> : launch_split<128, false, true>)
+                                      : (int8 ? launch_split<64, true, true> : launch_split<64, false, true>))
+                          : (d == 128 ? (int8 ? launch_split<128, true, false> : launch_split<128, false, false>)
+                                      : (int8 ? launch_split<64, true, false> : launch_split<64, false, false>));
+    st = split(a, after, err, stream);
     after = true;
   }
   if (st != TM_OK || p.slots == 1) return st;

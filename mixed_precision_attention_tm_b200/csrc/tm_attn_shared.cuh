@@ -57,6 +57,7 @@ struct SharedPlan {
   int group;                  // query heads per K/V head
   int own_tile, pre_tile;     // 1: on the tile kernel (256-row blocks), 0: on the split-key kernel (16-row blocks)
   int own_rows, pre_rows;     // row blocks per sequence, of the batch
+  int narrow;                 // split-key kernel: blocks of 8 rows, not 16
   int own_splits, pre_splits; // most results of a row
   int own_chunk;              // keys per split
   int fold;                   // key tiles of the prefix that the own tokens' row blocks go through first (no prefix results)
@@ -66,6 +67,10 @@ struct SharedPlan {
   int slots;                  // own_splits + pre_splits
   int64_t ml_bytes, bytes;    // workspace: (m, l) of every slot and row, then O
 };
+
+// Split-key kernel: rows of a block, and CTAs that an SM holds (their rings; INT8 at d = 128 in blocks of 16: registers).
+__host__ __device__ constexpr int split_block(bool narrow) { return narrow ? 8 : 16; }
+constexpr int split_resident(int d, bool int8, bool narrow) { return d == 64 || (int8 && narrow) ? 4 : int8 ? 3 : 2; }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
