@@ -184,7 +184,7 @@ struct SplitSmem {
   static constexpr int BYTES = OFF_BAR + kWarps * kStages * 8 + 16 + 1024;
 };
 
-// Attention of up to 16 packed rows over one range of keys.
+// Attention of up to 16 packed rows (NARROW: 8) over one range of keys.
 //
 // Decoding reads far more than it computes (a key's 2 d values serve g rows),
 // so this is built around the copies: each warp owns every fourth 16-key step
@@ -192,14 +192,21 @@ struct SplitSmem {
 // the end.  A warp's step is a chain of dependent
 // instructions, so it takes several warps to keep up with the copies: at
 // d = 128 in fp16 two CTAs (eight warps, 192 KB of rings) fit an SM, else
-// more.  With two warps of 32-key steps per CTA the same batch (64 sequences of 64 to
-// 1024 tokens, 143 MB) took 43 us.  A step's keys lie in one page, so a TMA copy
+// three or four.  Measured with 32 single tokens, 32 query heads over 8: behind
+// 16000 own tokens each, fp16, 2.1 GB in 299 us (7.0 TB/s, HBM's rate); INT8, 1.07
+// GB in 215 us (5.0 TB/s: the conversion's instructions); behind 200 to 2000,
+// where starts, ends and the join weigh, 144 MB in 30 us.  A step's keys lie in one page, so a TMA copy
 // brings its K (two at d = 128 in fp16), another its V, for a dozen
 // instructions where row copies took over a hundred.  A step that the range
 // ends in, or on a bad page, is copied row by row: rows past the end are zeros and
 // never read from memory.  The products run on mma.sync m16n8k16: 16 rows
 // hold a whole group of query heads, where a 128-row tensor-memory tile would
-// be nearly empty.
+// be nearly empty.  NARROW, for single tokens with up to eight query heads for a
+// K/V head, turns the products over: S^T = K Q^T and O^T = V^T P^T, keys and
+// dimensions on the 16 rows and the query rows on the 8 columns, with half the
+// MMAs, exponentials and sums (four INT8 CTAs on an SM, not three; behind 4000 own
+// tokens 77 -> 65 us in INT8, 83.5 -> 81.7 us in fp16).  P^T is the transpose of
+// S^T's fragments, one movmatrix for each 8 x 8.
 //
 // INT8: K and V stay codes in shared memory and become fp16 in registers
 // (exactly).  With t_j = s_j ks_j + log2 vs_j the weights 2^(t_j - m) carry

@@ -55,7 +55,7 @@ constexpr int kSplitBlockTiles = 3;
 
 struct SharedPlan {
   int group;                  // query heads per K/V head
-  int own_tile, pre_tile;     // 1: on the tile kernel (256-row blocks), 0: on the split-key kernel (16-row blocks)
+  int own_tile, pre_tile;     // 1: on the tile kernel (256-row blocks), 0: on the split-key kernel (16- or 8-row blocks)
   int own_rows, pre_rows;     // row blocks per sequence, of the batch
   int narrow;                 // split-key kernel: blocks of 8 rows, not 16
   int own_splits, pre_splits; // most results of a row

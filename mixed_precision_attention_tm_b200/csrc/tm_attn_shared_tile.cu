@@ -7,7 +7,7 @@
 // S(c + 2) follows P.V(c) into the half that P(c) leaves, so the next scores are
 // computed while the softmax works on the current ones.  O stays in tensor
 // memory over the whole range; a row's reference maximum is raised (and O
-// rescaled) only when a score exceeds it by 2^kLazy.
+// rescaled) only when a score exceeds it by 2^kLazyTile.
 //
 // Loads: one warp brings K and V with a TMA copy for each page (or 128 slots of
 // it) into the 128-byte-swizzled layout that the MMAs read, through a ring of
@@ -22,9 +22,18 @@
 // that is rounded, so that the scales add no rounding.  (V rounded to fp16
 // (code * scale) is a shared-memory pass less, and 1.2 times the error.)
 //
-// The prefix's work is one line of key tiles (row block by row block) cut into
-// equal pieces, one for each CTA, so that all SMs finish together; a CTA whose
+// The prefix's work is cut into equal pieces of key tiles, one for each SM, so
+// that all finish together: pieces of every row block where that divides well,
+// else of one line of key tiles, row block by row block, on which a CTA whose
 // piece crosses a row block's end writes one partial result for each block.
+//
+// Bounds, for a 64-key step of both tiles (d = 128): its MMAs take 1280 SM cycles (the
+// score products read Q from shared memory again for every 64 keys), its
+// exponentials on the special function unit alone 1024, the rest of the softmax a few hundred issue
+// slots of each warp; together 1460 to 1550 cycles, about 1.2 PFLOP/s (7200 packed
+// rows of 8 K/V heads behind 16384 positions: 405 us).  With few key tiles for a CTA
+// its start (setup, first copies, cold instructions: 5 us) and its results (128 KB)
+// count as much.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>

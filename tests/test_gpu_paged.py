@@ -331,6 +331,15 @@ def test_attention_groups(hq, hkv, int8):
     attend(21, [50, 200, 7], [2, 1, 3], 200, 64, 16, hq, hkv, int8)
 
 
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (6, 3), (7, 1), (16, 2), (9, 1)])
+@pytest.mark.parametrize("d,int8,scale", [(64, False, 2.0), (128, True, 2.0), (128, False, 30.0), (64, True, 0.0)])
+def test_attention_single_tokens_of_many_sequences(hq, hkv, d, int8, scale):
+    """Rows of eight query heads and fewer (and of nine), the shared prefix in blocks as small."""
+    lens = [0, 1, 15, 16, 17, 700, 128, 129] + [257 + 31 * i for i in range(16)]
+    attend(50, lens, [1] * len(lens), 100, d, 32, hq, hkv, int8, scale=scale, tail=1)
+    attend(51, lens, [0, 1, 1, 0] * 6, 0, d, 64, hq, hkv, int8, "head", scale=scale, causal=False)
+
+
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
 def test_attention_long_rows_and_many(d, int8):
