@@ -46,7 +46,8 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, bool int8,
   // CTAs per SM (32 sequences of up to 2000 tokens, INT8: 32.0 us, by waves 37.9).
   const bool many = own_blocks * own_units > 13 * kSmsB200;
   if (many) chunk = ceil_div(own_blocks * own_units + pre_blocks * pre_units, 5 * kSmsB200);
-  for (int64_t c = 1; !many && c <= 64; ++c) {
+  const int64_t longest = own_units > pre_units ? own_units : pre_units;
+  for (int64_t c = 1; !many && c <= 64 && (c == 1 || c <= longest); ++c) {
     const int64_t pre_ctas = pre_blocks * ceil_div(pre_units, c);
     const int64_t own_ctas = own_blocks * ceil_div((own_units * 6 + 9) / 10, c);
     const int64_t tenths = 10 * (pre_ctas + own_ctas) / resident;      // of a wave
