@@ -10,7 +10,7 @@
 // Every byte is read once and written once, so long prompts are bound by HBM
 // and single steps by latency.  Rotation of 16384 tokens, 32 + 8 heads of 128
 // (336 MB): 53.5 us, 0.96 of the measured copy bandwidth.  Norm and rotation of 8191
-// tokens, 32 + 8 heads of 64 (84 MB): 17.6 us, 0.73 of it.  Appending 9616 tokens to
+// tokens, 32 + 8 heads of 64 (84 MB): 16.3 us, 0.79 of it.  Appending 9616 tokens to
 // INT8 pages, 4 heads of 128 with 32 query heads rotated (187 MB): 41 us, 0.70 of it;
 // the codes' rounding and packing take issue slots.  64 tokens: 3.5 us, a chain of loads.
 //
@@ -81,11 +81,22 @@ enum { kNoCache = 0, kCacheF16 = 1, kCacheI8 = 2 };
 // layout (and the unrotated rest two by two), neighbours in the interleaved
 // one.  So the rotation needs no shuffles; the norm's sum takes log2(D / 16).
 // U items are loaded before the first is used, to keep loads in flight.
+//
+// Loads in flight against warps, in registers: one item ahead and seven blocks on
+// an SM for norms and for heads of 64 (norms of 4000 tokens, 32 + 8 heads of 128: 16.4
+// us, with two and six 19.8; 8191 of 64: 16.3 and 17.6), two and six for rotation alone
+// of heads of 128 (16384 tokens: 53.7 us, with one and seven 56.0) and for appending
+// (with three and five 59.5 to 60.1 us in one case, 73.1 to 70.4 in another).
+__host__ __device__ constexpr int items_ahead(int d, int cache, bool norm) {
+  return cache == kNoCache && (norm || d == 64) ? 1 : 2;
+}
+__host__ __device__ constexpr int blocks_held(int d, int cache, bool norm) { return 8 - items_ahead(d, cache, norm); }
+
 template <int D, int CACHE, bool NORM>
-__global__ void __launch_bounds__(kTokenWarps * 32, 6) token_kernel(const __grid_constant__ TokenArgs a, DevErr err) {
+__global__ void __launch_bounds__(kTokenWarps * 32, blocks_held(D, CACHE, NORM)) token_kernel(const __grid_constant__ TokenArgs a, DevErr err) {
   constexpr int LPR = D / 16;         // lanes of a head
   constexpr int RPW = 32 / LPR;       // heads of an item
-  constexpr int U = 2;
+  constexpr int U = items_ahead(D, CACHE, NORM);
   __shared__ __align__(16) float2 trig[kTokenWarps][64];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t job = static_cast<int64_t>(blockIdx.x) * kTokenWarps + warp;
@@ -303,7 +314,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32, 6) token_kernel(const __grid
 
 // Warps per token: enough of them for every SM to hold ten while a token has
 // items to share out; with many tokens one warp takes a token whole, so that its
-// sines and cosines are computed once.  An SM holds 24; with 28 each wave paid the
+// sines and cosines are computed once.  An SM holds 24 or 28; with 28 each wave paid the
 // chain before the first item again (1000 tokens, 32 + 8 heads of 128, with norms:
 // 9.3 us instead of 7.6; 2000 tokens, 16 + 4 heads, rotation alone: 7.9 and 5.6 us).
 int token_parts(int64_t T, int items) {
