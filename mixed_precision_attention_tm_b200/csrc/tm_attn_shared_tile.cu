@@ -265,6 +265,9 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
   // memory at the first __syncthreads, which it joins after its first copies.
   int u = unit;
   Segment sg{};
+  if (warp >= 8 && warp < 12) {
+  // One setmaxnreg for the four control warps: all of a warpgroup have to execute the same one.
+  regs_dec<C::CONTROL_REGS>();
   if (warp == 8) {
     if (lane == 0) {
       prefetch_tmap(&maps.q);
@@ -287,7 +290,6 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       fence_barrier_init();
     }
     __syncwarp();
-    regs_dec<C::CONTROL_REGS>();
     // ======================= loader =======================
     uint32_t n = 0, qn = 0;
     const int box_shift = shift < 7 ? shift : 7;       // key rows of a copy
@@ -420,94 +422,14 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
     for (uint32_t i = 2 * n > C::NSLOT ? 2 * n - C::NSLOT : 0; i < 2 * n; ++i)
       mbar_wait_warp(bar(LANDED + i % C::NSLOT), (i / C::NSLOT) & 1, err, &never);
   } else {
-  if (warp == 9) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
-    tc_fence_before();
-  }
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
-  if (INT8 && warp >= 12) {
-    // ======================= conversion of codes (warpgroup v: K or V; thread r: key row r of each tile) ====
-    regs_dec<C::CONVERT_REGS>();
-    const int v = (warp - 12) >> 2;
-    const int r = threadIdx.x & 127;
-    uint32_t i = v;
-    while (next_segment(u, sg)) {
-      const int nj = sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
-      // this row's page and scale, loaded two and one key tiles ahead
-      auto entry_of = [&](int j) { return j < nj ? entry_at(sg, sg.key0 + j * 128 + r) : -1; };
-      auto scales_at = [&](int j, int32_t page, __half& ks, __half& vs) {
-        ks = vs = __float2half(0.f);
-        if (!page_ok(page, a.pool.num_pages)) return;
-        const int64_t at = page * a.pool.sstride_page + (place(sg.key0 + j * 128 + r) & page_mask) * a.pool.sstride_t +
-                           sg.kvh * a.pool.sstride_h;
-        if (v == 0) ks = a.pool.ks[at];
-        vs = a.pool.vs[at];
-      };
-      int32_t entry = entry_of(0);
-      __half ks, vs, next_ks, next_vs;
-      scales_at(0, entry, next_ks, next_vs);
-      entry = entry_of(1);
-      for (int j = 0; j < nj; ++j, i += 2) {
-        ks = next_ks;
-        vs = next_vs;
-        scales_at(j + 1, entry, next_ks, next_vs);
-        entry = entry_of(j + 2);
-        {
-          const uint32_t slot = i % C::NSLOT;
-          mbar_wait_warp(bar(T_CODES + slot), (i / C::NSLOT) & 1, err, abort_flag);
-          const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT;
-          // The scales outlive K's slot: the softmax reads those of key tile j until P(2 j + 1).  With one stage more
-          // than the ring has key tiles, the next tile in this stage lands behind a release of key tile j + 1, whose
-          // last S is issued behind P.V(2 j + 1).
-          const uint32_t bits = __float_as_uint(__half2float(vs));
-          if (v == 0) {
-            float* sc = scales + ((i / 2) % C::STAGES) * 256 + r;
-            sc[0] = __half2float(ks);
-            sc[128] = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);      // 1 <= |f| < 2; of a zero scale: 1
-          }
-          const __half2 by = __half2half2(__float2half(v ? __uint_as_float(bits & 0x7f800000u) : 1.f));
-          auto widen = [&](uint4 c, uint32_t at, int q) {      // 16 codes to pieces 2 q and 2 q + 1 of a row
-            const uint32_t x[4] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u};
-            sts128(at + (((2 * q) ^ (r & 7)) << 4),
-                   make_uint4(scaled2(x[0], 0x4140u, by), scaled2(x[0], 0x4342u, by), scaled2(x[1], 0x4140u, by),
-                              scaled2(x[1], 0x4342u, by)));
-            sts128(at + (((2 * q + 1) ^ (r & 7)) << 4),
-                   make_uint4(scaled2(x[2], 0x4140u, by), scaled2(x[2], 0x4342u, by), scaled2(x[3], 0x4140u, by),
-                              scaled2(x[3], 0x4342u, by)));
-          };
-          if (D == 128) {
-            // The codes lie where the upper 64 columns go, row r's in row r's place; there piece q's output covers
-            // code pieces up to q, which have been read.  A rolled loop: the softmax needs the instruction cache.
-            const uint32_t src = tile + C::HALF + r * 128;
-            uint4 c = lds128(src + ((r & 7) << 4));
-#pragma unroll 1
-            for (int q = 0; q < 8; ++q) {
-              const uint4 after = lds128(src + ((((q + 1) & 7) ^ (r & 7)) << 4));
-              widen(c, tile + (q >> 2) * C::HALF + r * 128, q & 3);
-              c = after;
-            }
-          } else {
-            // 64-byte rows over other rows' places: all are read before any is written
-            const uint32_t src = tile + C::CODES + r * 64;
-            uint4 c[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) c[q] = lds128(src + ((q ^ ((r >> 1) & 3)) << 4));
-            named_bar_sync(NB_CVT + v, 128);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) widen(c[q], tile + r * 128, q);
-          }
-          fence_async_shared();    // read by tcgen05.mma
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(T_FULL + slot));
-        }
-      }
+    if (warp == 9) {
+      tmem_alloc(smem_u32(tmem_slot), 512);
+      tmem_relinquish();
+      tc_fence_before();
     }
-  } else if (warp >= 8) {
-    regs_dec<C::CONTROL_REGS>();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
     if (warp == 9 || warp == 10) {
       // ======================= tcgen05 issuers (warp 9: tile A, warp 10: tile B) ====
       // They never touch shared memory: the wait helper polls for them.
@@ -622,6 +544,89 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           if (j == na - 1 || j == nb - 1) wait_slot(2 * n + 1);
           if (j == na - 1) handoff(0);
           if (j == nb - 1) handoff(1);
+        }
+      }
+    }
+  }
+  } else {
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (INT8 && warp >= 12) {
+    // ======================= conversion of codes (warpgroup v: K or V; thread r: key row r of each tile) ====
+    regs_dec<C::CONVERT_REGS>();
+    const int v = (warp - 12) >> 2;
+    const int r = threadIdx.x & 127;
+    uint32_t i = v;
+    while (next_segment(u, sg)) {
+      const int nj = sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
+      // this row's page and scale, loaded two and one key tiles ahead
+      auto entry_of = [&](int j) { return j < nj ? entry_at(sg, sg.key0 + j * 128 + r) : -1; };
+      auto scales_at = [&](int j, int32_t page, __half& ks, __half& vs) {
+        ks = vs = __float2half(0.f);
+        if (!page_ok(page, a.pool.num_pages)) return;
+        const int64_t at = page * a.pool.sstride_page + (place(sg.key0 + j * 128 + r) & page_mask) * a.pool.sstride_t +
+                           sg.kvh * a.pool.sstride_h;
+        if (v == 0) ks = a.pool.ks[at];
+        vs = a.pool.vs[at];
+      };
+      int32_t entry = entry_of(0);
+      __half ks, vs, next_ks, next_vs;
+      scales_at(0, entry, next_ks, next_vs);
+      entry = entry_of(1);
+      for (int j = 0; j < nj; ++j, i += 2) {
+        ks = next_ks;
+        vs = next_vs;
+        scales_at(j + 1, entry, next_ks, next_vs);
+        entry = entry_of(j + 2);
+        {
+          const uint32_t slot = i % C::NSLOT;
+          mbar_wait_warp(bar(T_CODES + slot), (i / C::NSLOT) & 1, err, abort_flag);
+          const uint32_t tile = sbase + C::OFF_SLOT + slot * C::SLOT;
+          // The scales outlive K's slot: the softmax reads those of key tile j until P(2 j + 1).  With one stage more
+          // than the ring has key tiles, the next tile in this stage lands behind a release of key tile j + 1, whose
+          // last S is issued behind P.V(2 j + 1).
+          const uint32_t bits = __float_as_uint(__half2float(vs));
+          if (v == 0) {
+            float* sc = scales + ((i / 2) % C::STAGES) * 256 + r;
+            sc[0] = __half2float(ks);
+            sc[128] = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);      // 1 <= |f| < 2; of a zero scale: 1
+          }
+          const __half2 by = __half2half2(__float2half(v ? __uint_as_float(bits & 0x7f800000u) : 1.f));
+          auto widen = [&](uint4 c, uint32_t at, int q) {      // 16 codes to pieces 2 q and 2 q + 1 of a row
+            const uint32_t x[4] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u};
+            sts128(at + (((2 * q) ^ (r & 7)) << 4),
+                   make_uint4(scaled2(x[0], 0x4140u, by), scaled2(x[0], 0x4342u, by), scaled2(x[1], 0x4140u, by),
+                              scaled2(x[1], 0x4342u, by)));
+            sts128(at + (((2 * q + 1) ^ (r & 7)) << 4),
+                   make_uint4(scaled2(x[2], 0x4140u, by), scaled2(x[2], 0x4342u, by), scaled2(x[3], 0x4140u, by),
+                              scaled2(x[3], 0x4342u, by)));
+          };
+          if (D == 128) {
+            // The codes lie where the upper 64 columns go, row r's in row r's place; there piece q's output covers
+            // code pieces up to q, which have been read.  A rolled loop: the softmax needs the instruction cache.
+            const uint32_t src = tile + C::HALF + r * 128;
+            uint4 c = lds128(src + ((r & 7) << 4));
+#pragma unroll 1
+            for (int q = 0; q < 8; ++q) {
+              const uint4 after = lds128(src + ((((q + 1) & 7) ^ (r & 7)) << 4));
+              widen(c, tile + (q >> 2) * C::HALF + r * 128, q & 3);
+              c = after;
+            }
+          } else {
+            // 64-byte rows over other rows' places: all are read before any is written
+            const uint32_t src = tile + C::CODES + r * 64;
+            uint4 c[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) c[q] = lds128(src + ((q ^ ((r >> 1) & 3)) << 4));
+            named_bar_sync(NB_CVT + v, 128);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) widen(c[q], tile + r * 128, q);
+          }
+          fence_async_shared();    // read by tcgen05.mma
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(T_FULL + slot));
         }
       }
     }
