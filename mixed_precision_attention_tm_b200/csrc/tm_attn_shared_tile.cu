@@ -641,6 +641,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
     uint32_t cc = 0;      // chunks of this query tile so far, over all segments
     uint32_t n = 0;       // key tiles so far
     uint32_t segs = 0;    // segments of this query tile so far
+    bool owed = false;    // tile 0: the other warpgroup's arrival for its last turn has not been met
     const int64_t total = a.T * Hq;
     const bool direct = p.slots == 1;
     while (next_segment(u, sg)) {
@@ -656,6 +657,8 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       float m_used = -INFINITY, l = 0.f;
       // The two softmax warpgroups take turns at their exponentials: side by side they would slow each other down
       // into lockstep, and stores, waits and handoffs of both would leave the SM idle at the same time.
+      // Strictly in turns, over segments' ends too: tile 0 meets tile 1's last arrival before its next first turn.
+      // (An arrival that ran ahead would complete a barrier that tile 1 has not come to, and leave it there.)
       const int turns = 2 * min(sg.nj[0], sg.nj[1]);
       for (int c = 0; c < 2 * nt; ++c, ++cc) {
         const int sl = c & 1;
@@ -696,7 +699,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
             m_used = mt;
           }
         }
-        if (c < turns && (t == 1 || c > 0)) named_bar_sync(NB_TURN + t, 256);
+        if (c < turns && (t == 1 || c > 0 || owed)) named_bar_sync(NB_TURN + t, 256);
         const float msub = (m_used == -INFINITY) ? 0.f : m_used - kPOffset;
         const uint64_t c2 = f2pack(cs, cs), nm2 = f2pack(-msub, -msub);
         uint32_t pk[HN / 2];
@@ -726,7 +729,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           f2unpack(s2, s0, s1);
           l = l * alpha + (s0 + s1);
         }
-        if (c < turns && (t == 0 || c + 1 < turns)) named_bar_arrive(NB_TURN + 1 - t, 256);
+        if (c < turns) named_bar_arrive(NB_TURN + 1 - t, 256);
         __syncwarp();
         tmem_st32p(s_c, pk);      // P(c) over the first 32 columns of its half
         // P.V(c - 1) must have completed before O is rescaled; phases up to
@@ -757,6 +760,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         // not waiting: this half's next P follows an S that is issued behind this one's P.V
         named_bar_arrive(NB_P + 2 * t + sl, 160);
       }
+      if (turns > 0) owed = t == 0;
       n += sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
 
       // ---- the row's result: partial (O, m, l), or the output
@@ -822,6 +826,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         tc_fence_before();      // these reads of O come before the next segment's first P.V
       }
     }
+    if (owed) named_bar_sync(NB_TURN + t, 256);
   }
   }
 

@@ -18,3 +18,73 @@ def test_tile_kernel_warpgroups_change_registers_together():
     assert len(re.findall(r"regs_dec<C::CONTROL_REGS>\(\)", text)) == 1
     assert re.search(r"if \(warp >= 8 && warp < 12\) \{\n(\s*//[^\n]*\n)*\s*regs_dec<C::CONTROL_REGS>\(\);\n\s*if \(warp == 8\)", text)
     assert len(re.findall(r"regs_(?:dec|inc)<", text)) == 3
+
+
+def turn_program(t, segments, sync, arrive, last):
+    """What softmax warpgroup t does at the turn barriers, over segments of so many turns each."""
+    steps, owed = [], False
+    for turns in segments:
+        for c in range(turns):
+            at = dict(c=c, t=t, turns=turns, owed=owed)
+            if eval(sync, {}, at):
+                steps.append(("sync", t))
+            if eval(arrive, {}, at):
+                steps.append(("arrive", 1 - t))
+        if turns:
+            owed = t == 0
+        steps.append(("results", t))
+    if last and owed:
+        steps.append(("sync", t))
+    return steps
+
+
+def turn_faults(programs):
+    """Every order of the two warpgroups' steps over barriers that complete with two arrivals, whoever's."""
+    faults, seen, todo = set(), set(), [((0, 0), ((), ()), (False, False))]
+    while todo:
+        state = todo.pop()
+        if state in seen:
+            continue
+        seen.add(state)
+        at, bars, waits = state
+        moved = False
+        for w in (0, 1):
+            if waits[w] or at[w] == len(programs[w]):
+                continue
+            moved = True
+            kind, b = programs[w][at[w]]
+            at2, bars2, waits2 = list(at), [list(x) for x in bars], list(waits)
+            if kind != "results":
+                bars2[b].append((w, kind))
+            if kind == "sync":
+                waits2[w] = True
+            else:
+                at2[w] += 1
+            if kind != "results" and len(bars2[b]) == 2:
+                if {x for x, _ in bars2[b]} != {0, 1}:
+                    faults.add("one warpgroup's arrivals complete a barrier")
+                for x, k in bars2[b]:
+                    if k == "sync":
+                        waits2[x] = False
+                        at2[x] += 1
+                bars2[b] = []
+            todo.append((tuple(at2), tuple(tuple(x) for x in bars2), tuple(waits2)))
+        if not moved and (any(waits) or any(at[w] < len(programs[w]) for w in (0, 1))):
+            faults.add("stuck")
+        elif not moved and any(bars):
+            faults.add("an arrival is left over")
+    return faults
+
+
+def test_tile_kernel_turns_over_several_segments():
+    """The conditions of the kernel's turn barriers, in every order in which the two warpgroups may come to them."""
+    text = source("tm_attn_shared_tile.cu")
+
+    def conditions(call):
+        return [c.replace("&&", "and").replace("||", "or")
+                for c in re.findall(r"if \((.+)\) named_bar_" + call + r", 256\);", text)]
+    syncs, arrives = conditions(r"sync\(NB_TURN \+ t"), conditions(r"arrive\(NB_TURN \+ 1 - t")
+    assert len(arrives) == 1 and syncs[1:] in ([], ["owed"])
+    for segments in ([2], [2, 2], [4, 2, 0, 2], [0, 2, 0, 4], [2, 0, 0, 2, 2]):
+        programs = [turn_program(t, segments, syncs[0], arrives[0], len(syncs) == 2) for t in (0, 1)]
+        assert turn_faults(programs) == set(), segments
