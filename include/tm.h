@@ -614,9 +614,10 @@ tm_status tm_kv_gather(const tm_paged_kv* cache, const int32_t* table, int64_t t
  *   out = fp16( sum_j softmax_j(q . k_j / sqrt(d)) v_j )
  * fp32 scores, statistics and sums; P rounded to fp16 for the P.V product, the
  * one rounding besides the result's (INT8 scales are applied in fp32).  A
- * row that sees nothing is 0; rows behind the last sequence are left as they
- * were.  Values at visible and causally hidden positions below kv_lens[b] must
- * be finite; the rest of a page is never used.
+ * row that sees nothing is 0, one whose query holds a NaN or an infinity else
+ * NaN; rows behind the last sequence are left as they were.  Values at visible
+ * and causally hidden positions below kv_lens[b] must be finite; the rest of a
+ * page is never used.
  *   q, out: fp16 [T, Hq, d], Hq a multiple of the cache's H; out may be q.
  *   prefix_len = 0: plain paged attention (prefix_pages may be NULL).
  *   max_seqlen: bound on n_b (ignored without cu_seqlens); max_kv_len: bound

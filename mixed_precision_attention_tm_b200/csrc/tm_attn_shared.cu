@@ -653,6 +653,8 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
   cp_wait<0>();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    // a row that saw keys, all of them at -inf (its query is not finite): 0 / 0, not a row that saw nothing
+    if (lim[h] > first && m[h] == -INFINITY) l[h] = NAN;
     for (int w = NARROW ? 4 : 1; w < (NARROW ? 32 : 4); w *= 2) l[h] += __shfl_xor_sync(0xffffffffu, l[h], w);
   }
 

@@ -146,6 +146,27 @@ __device__ __forceinline__ uint32_t scaled2(uint32_t w, uint32_t sel, __half2 by
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// row_max, NaN where any value is
+__device__ __forceinline__ float nan_max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ float nan_row_max(const float* x) {
+  static_assert(N == 64, "eight values behind each of eight chains");
+  float a[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    a[k] = x[k];
+#pragma unroll
+    for (int t = 1; t < 7; t += 2) a[k] = nan_max3(a[k], x[k + 8 * t], x[k + 8 * (t + 1)]);
+    a[k] = nan_max3(a[k], x[k + 56], x[k + 56]);
+  }
+  a[0] = nan_max3(a[0], a[1], a[2]);
+  return nan_max3(a[0], nan_max3(a[3], a[4], a[5]), nan_max3(a[6], a[7], a[7]));
+}
+
 struct TileMaps {
   CUtensorMap q;
   int q_tma;          // Q through its map: 128 rows are whole tokens
@@ -655,6 +676,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       int lim_own = fold;
       if (row_ok && !prefix) lim_own += max(0, a.causal ? min(sg.lk, sg.hidden + tok_in) : sg.lk);
       float m_used = -INFINITY, l = 0.f;
+      bool saw = false;      // a key
       // The two softmax warpgroups take turns at their exponentials: side by side they would slow each other down
       // into lockstep, and stores, waits and handoffs of both would leave the SM idle at the same time.
       // Strictly in turns, over segments' ends too: tile 0 meets tile 1's last arrival before its next first turn.
@@ -693,8 +715,9 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         }
         float alpha = 1.f;
         if (nv > 0) {
-          const float mt = row_max<HN>(x) * cs;
-          if (mt > m_used + kLazyTile<INT8>) {
+          const float mt = nan_row_max<HN>(x) * cs;
+          saw = true;
+          if (!(mt <= m_used + kLazyTile<INT8>)) {      // a NaN too: alpha, and with it l, is NaN from there on
             alpha = ex2_approx(m_used - mt);
             m_used = mt;
           }
@@ -764,7 +787,10 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       n += sg.nj[0] > sg.nj[1] ? sg.nj[0] : sg.nj[1];
 
       // ---- the row's result: partial (O, m, l), or the output
-      if (m_used == -INFINITY) l = 0.f;      // a row that saw nothing
+      // A row that saw nothing has no weight.  Of a query that is not finite all scores are NaN or infinities: NaN, which
+      // the weights alone need not show (the exponentials on the FMA pipe clamp a NaN to 2^-125).
+      if (!saw) l = 0.f;
+      else if (!(fabsf(m_used) < INFINITY)) l = NAN;
       if (nt > 0) {
         mbar_wait(bar(T_OLAST + t), segs & 1, err, abort_flag);
         ++segs;
