@@ -126,9 +126,11 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStep = 16;     // keys of one warp step: never more than one page
 constexpr int kStages = 3;
-// 2^kPOffset is the largest weight when the reference is the maximum; scores up
-// to 2^kLazy above it leave it alone: 2^15 at most, inside fp16.
-constexpr float kLazy = 15.0f - kPOffset;
+// 2^kPOffset is the largest weight when the reference is the maximum; scores
+// above it leave it alone up to this exponent: 2^15 at most, inside fp16.  (What
+// counts is the exponent as it is computed: 2^24 and more from zero, a score
+// and a reference have steps of 2 and more.)
+constexpr float kTop = 15.0f;
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -547,13 +549,13 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
         }
       }
     }
-    // the references are raised (and O and l rescaled) only when a score exceeds one by 2^kLazy
+    // the references are raised (and O and l rescaled) only when a weight would exceed 2^kTop
     float mx[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       mx[h] = NARROW ? fmaxf(x[0][h], x[1][h])
                      : fmaxf(fmaxf(x[0][XE / 2 * h], x[0][XE / 2 * h + 1]), fmaxf(x[1][XE / 2 * h], x[1][XE / 2 * h + 1]));
-    if (__any_sync(0xffffffffu, mx[0] > m[0] + kLazy || mx[1] > m[1] + kLazy)) {
+    if (__any_sync(0xffffffffu, mx[0] - (m[0] - kPOffset) > kTop || mx[1] - (m[1] - kPOffset) > kTop)) {
       float scale[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {

@@ -7,7 +7,7 @@
 // S(c + 2) follows P.V(c) into the half that P(c) leaves, so the next scores are
 // computed while the softmax works on the current ones.  O stays in tensor
 // memory over the whole range; a row's reference maximum is raised (and O
-// rescaled) only when a score exceeds it by 2^kLazyTile.
+// rescaled) only when a weight would exceed 2^kTopTile.
 //
 // Loads: one warp brings K and V with a TMA copy for each page (or 128 slots of
 // it) into the 128-byte-swizzled layout that the MMAs read, through a ring of
@@ -47,10 +47,16 @@ namespace tmk {
 namespace {
 
 // 2^kPOffset is the largest weight when the reference is the maximum; scores
-// up to 2^kLazyTile above it are left alone: 2^15 at most, inside fp16, with what
-// INT8 V scales multiply in (less than 2).
+// above it are left alone up to this exponent: 2^15 at most, inside fp16, with
+// what INT8 V scales multiply in (less than 2).
 template <bool INT8>
-constexpr float kLazyTile = (INT8 ? 14.0f : 15.0f) - kPOffset;
+constexpr float kTopTile = INT8 ? 14.0f : 15.0f;
+
+// An exponent is one FMA of a score product while scores are below this, in
+// powers of two (its unrounded product and the reference then differ by an
+// eighth at most; fp16 leaves a half above 2^15); from there on both come from
+// the same rounded product.  fp16 scores reach 2^36.
+constexpr float kLargeScore = 4194304.0f;
 
 // Of every 8 pairs of exponentials, how many run on the FMA pipe: the special
 // function unit alone takes as long as the MMAs of a tile.  A 64-key step of both
@@ -706,21 +712,27 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
             f2unpack(f2mul(f2pack(x[e + 2], x[e + 3]), f2pack(k4.z, k4.w)), x[e + 2], x[e + 3]);
           }
         }
-        const float cs = a.scale_log2;
+        float cs = a.scale_log2;
         const int key0 = sg.key0 + c * HN;
         const int nv = max(0, min((key0 < fold ? lim_prefix : lim_own) - key0, HN));
         if (!__all_sync(0xffffffffu, nv == HN)) {
 #pragma unroll
           for (int e = 0; e < HN; ++e) x[e] = (e < nv) ? x[e] : -INFINITY;
         }
-        float alpha = 1.f;
+        float alpha = 1.f, mt = 0.f;
         if (nv > 0) {
-          const float mt = nan_row_max<HN>(x) * cs;
+          mt = nan_row_max<HN>(x) * cs;
           saw = true;
-          if (!(mt <= m_used + kLazyTile<INT8>)) {      // a NaN too: alpha, and with it l, is NaN from there on
+          // a NaN too: alpha, and with it l, is NaN from there on
+          if (mt - (m_used - kPOffset) > kTopTile<INT8> || mt != mt) {
             alpha = ex2_approx(m_used - mt);
             m_used = mt;
           }
+        }
+        if (__any_sync(0xffffffffu, fabsf(mt) > kLargeScore)) {
+#pragma unroll
+          for (int e = 0; e < HN; ++e) x[e] *= cs;
+          cs = 1.f;
         }
         if (c < turns && (t == 1 || c > 0 || owed)) named_bar_sync(NB_TURN + t, 256);
         const float msub = (m_used == -INFINITY) ? 0.f : m_used - kPOffset;

@@ -58,3 +58,91 @@ def test_queries_that_are_not_finite(lens, new, prefix, d, int8):
         assert bool(got[bad & ~nothing].isnan().all())
         assert bool((got[nothing] == 0).all())
         base.within(got[~bad], want[~bad], tol[~bad])
+
+
+# As QUERIES: tiles written directly, joined, with the prefix folded in, with a pass for it; split-key kernel, one piece and several.
+PATHS = [
+    ([100, 90], [100, 90], 0), ([2500, 100], [100, 100], 0), ([200, 64], [70, 64], 300),
+    ([20 + i for i in range(70)], [1 + i % 11 for i in range(70)], 2304), ([70, 200], [1, 2], 0), ([70, 2000], [1, 1], 700),
+]
+
+
+def fill_keys(kv, keys):
+    """Sets a pool's keys (one fp16 row for each slot, heads alike), quantised where its pages are INT8."""
+    k = keys[:, :, None].expand(*keys.shape[:2], kv.H, kv.d)
+    if kv.int8:
+        codes, scales = ref.quantise(k.cpu().double())
+        kv.k.copy_(codes), kv.k_scales.copy_(scales)
+    else:
+        kv.k.copy_(k)
+
+
+@pytest.mark.parametrize("d,int8", [(128, False), (128, True), (64, False), (64, True)])
+@pytest.mark.parametrize("size", [2.0 ** 5, 2.0 ** 12, 2.0 ** 15])
+@pytest.mark.parametrize("lens,new,prefix", PATHS)
+def test_scores_up_to_the_end_of_fp16(lens, new, prefix, size, d, int8):
+    """Queries and keys up to the largest fp16 numbers, scores up to 2^36: of levels 2^-3 apart and more the highest one
+    that a row sees takes all, so the result is the mean of its values."""
+    hq, hkv, page = 4, 2, 64
+    g = base.gen(63)
+    table, shared, total = base.make_table(63, lens, page, extra=prefix)
+    kv = base.make_pool(g, total, page, hkv, d, int8)
+    level = torch.randint(-8, 9, (total, page, 1), generator=g, device="cuda").float() / 8
+    fill_keys(kv, (level * size).half().expand(total, page, d))
+    q = torch.full((sum(new), hq, d), size, dtype=torch.float16, device="cuda")
+    q[::3] *= 1.5                                # 49152 at the most
+    args = dict(prefix_pages=shared, prefix_len=prefix, cu_seqlens=base.offsets(new), max_seqlen=max(new))
+    got = ops.attn_shared_prefix(q, kv, table, base.i32(lens), **args)
+    base.ok()
+    k, v = base.values(kv)
+    # The sums are exact or off by 2^-17 of themselves, the levels 2^-3: only the highest counts (2^5: 2^10 sqrt(d) / 8 powers
+    # of two and more between levels).  Its equal weights are rounded once each, INT8's with the V scale, and summed.
+    pages = [] if shared is None else shared.cpu().tolist()
+    want, _ = ref.attention(q, (k, v), table.cpu(), lens, new, pages, prefix)
+    size_of, _ = ref.attention(q, (k, v.abs()), table.cpu(), lens, new, pages, prefix)
+    tol = size_of * (2 * ref.HALF + (prefix + max(lens)) * 2.0 ** -24 + 2.0 ** -16) + ref.TINY
+    if not int8 or PATHS.index((lens, new, prefix)) < 3:
+        base.within(got, want, tol)
+        return
+    # The split-key kernel rounds t = score + log2(V scale) to fp32 once and divides a weight 2^t by the scale again in
+    # the row's sum: equal scores of 2^13 and more get weights that differ by up to 2^(step of t), the same in both
+    # sums.  The result is some mean of the same values: between the least and the largest of them.
+    got, t0 = got.cpu().double(), 0
+    for b, n in enumerate(new):
+        kb, vb = (torch.cat((ref.rows_of(x, pages, prefix), ref.rows_of(x, table[b].cpu(), lens[b]))) for x in (k, v))
+        for i in range(n):
+            end = prefix + lens[b] - n + i + 1
+            best = kb[:end, 0, 0] == kb[:end, 0, 0].max()
+            top = vb[:end][best].repeat_interleave(hq // hkv, 1)
+            slack = tol[t0 + i] + top.abs().amax(0) * 2 * ref.HALF
+            assert bool(((got[t0 + i] <= top.amax(0) + slack) & (got[t0 + i] >= top.amin(0) - slack)).all())
+        t0 += n
+
+
+@pytest.mark.parametrize("d,int8", [(128, False), (128, True), (64, False), (64, True)])
+@pytest.mark.parametrize("lens,new,prefix", PATHS)
+def test_near_scores_far_from_zero_stay_weights(lens, new, prefix, d, int8):
+    """Scores a few units apart at 2^22 and further on, where a unit is below fp32's step: whatever their rounding, a
+    result is a mean of the values that a row sees."""
+    hq, hkv, page = 4, 2, 64
+    g = base.gen(64)
+    table, shared, total = base.make_table(64, lens, page, extra=prefix)
+    kv = base.make_pool(g, total, page, hkv, d, int8)
+    keys = torch.zeros(total, page, d, device="cuda")
+    q = torch.zeros(sum(new), hq, d, dtype=torch.float16, device="cuda")
+    # a large product that all keys share, and small ones: 2^21 .. 2^33 in all, 16 apart
+    keys[..., 0], q[..., 0] = 2.0 ** 12, (2.0 ** torch.arange(9, 16, device="cuda")).half()[torch.arange(sum(new)) % 7, None]
+    keys[..., 1], q[..., 1] = torch.randint(0, 64, (total, page), generator=g, device="cuda").float() * 64, 1.0 / 4
+    keys[..., 2:6], q[..., 2:6] = 2.0 ** 13, (2.0 ** torch.arange(9, 16, device="cuda")).half()[torch.arange(sum(new)) % 7, None, None]
+    fill_keys(kv, keys.half())
+    args = dict(prefix_pages=shared, prefix_len=prefix, cu_seqlens=base.offsets(new), max_seqlen=max(new))
+    got = ops.attn_shared_prefix(q, kv, table, base.i32(lens), **args).cpu()
+    base.ok()
+    v = base.values(kv)[1]
+    t0 = 0
+    for b, n in enumerate(new):
+        vb = torch.cat((ref.rows_of(v, [] if shared is None else shared.cpu(), prefix), ref.rows_of(v, table[b].cpu(), lens[b])))
+        vb = vb.repeat_interleave(hq // hkv, 1)
+        slack = vb.abs().amax(0) * (3 * ref.HALF)      # the weights' roundings against their sum, and the result's
+        assert bool(((got[t0:t0 + n] <= vb.amax(0) + slack) & (got[t0:t0 + n] >= vb.amin(0) - slack)).all())
+        t0 += n
