@@ -52,11 +52,18 @@ namespace {
 template <bool INT8>
 constexpr float kTopTile = INT8 ? 14.0f : 15.0f;
 
-// An exponent is one FMA of a score product while scores are below this, in
-// powers of two (its unrounded product and the reference then differ by an
-// eighth at most; fp16 leaves a half above 2^15); from there on both come from
-// the same rounded product.  fp16 scores reach 2^36.
-constexpr float kLargeScore = 4194304.0f;
+// An exponent is one FMA of an unrounded score product, a reference rounded:
+// they differ by up to half of fp32's step there, which up to this distance from
+// zero (in powers of two; fp16 scores reach 2^36) is at most 4.  Further on a
+// row's products are taken with a power of two instead of log2(e) / sqrt(d) and
+// are exact.  There different fp32 scores lie at least 8 powers of two apart, so
+// that what such a row loses is a lesser weight's size: 2^-8 may count as 2^-8.2
+// (d = 128), 2^-11.5 as 2^-16 (d = 64).  Rounding each product for these rows instead
+// took a branch before the exponentials (16 chunks of prompts behind 16384 positions: 551 us
+// a call instead of 540 to 547).
+constexpr float kFarScore = 134217728.0f;
+template <int D>
+constexpr float kFarScale = D == 128 ? 0.125f : 0.25f;
 
 // Of every 8 pairs of exponentials, how many run on the FMA pipe: the special
 // function unit alone takes as long as the MMAs of a tile.  A 64-key step of both
@@ -681,7 +688,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       const int lim_prefix = row_ok ? prefix_len : 0;
       int lim_own = fold;
       if (row_ok && !prefix) lim_own += max(0, a.causal ? min(sg.lk, sg.hidden + tok_in) : sg.lk);
-      float m_used = -INFINITY, l = 0.f;
+      float x_ref = -INFINITY, l = 0.f;      // reference: a score product of the row
       bool saw = false;      // a key
       // The two softmax warpgroups take turns at their exponentials: side by side they would slow each other down
       // into lockstep, and stores, waits and handoffs of both would leave the SM idle at the same time.
@@ -712,31 +719,29 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
             f2unpack(f2mul(f2pack(x[e + 2], x[e + 3]), f2pack(k4.z, k4.w)), x[e + 2], x[e + 3]);
           }
         }
-        float cs = a.scale_log2;
+        const float cs = a.scale_log2;
         const int key0 = sg.key0 + c * HN;
         const int nv = max(0, min((key0 < fold ? lim_prefix : lim_own) - key0, HN));
         if (!__all_sync(0xffffffffu, nv == HN)) {
 #pragma unroll
           for (int e = 0; e < HN; ++e) x[e] = (e < nv) ? x[e] : -INFINITY;
         }
-        float alpha = 1.f, mt = 0.f;
+        // row's factor, and what its products are taken from: x * factor - less is the exponent
+        auto factor_of = [&]() { return fabsf(x_ref * cs) > kFarScore ? kFarScale<D> : cs; };
+        float alpha = 1.f, factor = factor_of(), less = __fsub_rn(__fmul_rn(x_ref, factor), kPOffset);
         if (nv > 0) {
-          mt = nan_row_max<HN>(x) * cs;
+          const float top = nan_row_max<HN>(x);
           saw = true;
-          // a NaN too: alpha, and with it l, is NaN from there on
-          if (mt - (m_used - kPOffset) > kTopTile<INT8> || mt != mt) {
-            alpha = ex2_approx(m_used - mt);
-            m_used = mt;
+          if (!(fmaf(top, factor, -less) <= kTopTile<INT8>)) {      // a NaN too: alpha, and with it l, is NaN from there on
+            alpha = ex2_approx((x_ref - top) * cs);
+            x_ref = top;
+            factor = factor_of();
+            less = __fsub_rn(__fmul_rn(x_ref, factor), kPOffset);
           }
         }
-        if (__any_sync(0xffffffffu, fabsf(mt) > kLargeScore)) {
-#pragma unroll
-          for (int e = 0; e < HN; ++e) x[e] *= cs;
-          cs = 1.f;
-        }
         if (c < turns && (t == 1 || c > 0 || owed)) named_bar_sync(NB_TURN + t, 256);
-        const float msub = (m_used == -INFINITY) ? 0.f : m_used - kPOffset;
-        const uint64_t c2 = f2pack(cs, cs), nm2 = f2pack(-msub, -msub);
+        if (x_ref == -INFINITY) less = 0.f;
+        const uint64_t c2 = f2pack(factor, factor), nm2 = f2pack(-less, -less);
         uint32_t pk[HN / 2];
         uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -802,7 +807,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       // A row that saw nothing has no weight.  Of a query that is not finite all scores are NaN or infinities: NaN, which
       // the weights alone need not show (the exponentials on the FMA pipe clamp a NaN to 2^-125).
       if (!saw) l = 0.f;
-      else if (!(fabsf(m_used) < INFINITY)) l = NAN;
+      else if (!(fabsf(x_ref) < INFINITY)) l = NAN;
       if (nt > 0) {
         mbar_wait(bar(T_OLAST + t), segs & 1, err, abort_flag);
         ++segs;
@@ -810,7 +815,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         __syncwarp();
       }
       const int64_t idx = static_cast<int64_t>(tok) * Hq + head;
-      if (row_ok && !direct) a.ml[sg.slot * total + idx] = make_float2(m_used, l);
+      if (row_ok && !direct) a.ml[sg.slot * total + idx] = make_float2(x_ref * a.scale_log2, l);
       const float inv = !direct ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
       if (nt > 0 || direct) {
         // OUT_COLS columns of the warp's 32 rows at a time through shared memory, so that a store instruction writes
