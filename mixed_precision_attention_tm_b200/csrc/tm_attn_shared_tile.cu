@@ -17,8 +17,9 @@
 //
 // INT8 pages: the copies bring the codes, which two more warpgroups (one
 // for K, one for V) turn into fp16 in place, exactly: K stays codes, V is code
-// times the largest power of two in its scale.  A key's K scale multiplies its
-// scores in fp32 and the rest of its V scale (between 1 and 2) its weight before
+// times the largest power of two in its scale, up to 2^8 (a code is 128 at most:
+// fp16 holds 2^15).  A key's K scale multiplies its scores in fp32 and the rest of
+// its V scale (between 1 and 2, of scales from 512 on up to 256) its weight before
 // that is rounded, so that the scales add no rounding.  (V rounded to fp16
 // (code * scale) is a shared-memory pass less, and 1.2 times the error.)
 //
@@ -48,12 +49,13 @@ namespace {
 
 // 2^kPOffset is the largest weight when the reference is the maximum; scores
 // above it are left alone up to this exponent: 2^15 at most, inside fp16, with
-// what INT8 V scales multiply in (less than 2).
+// what INT8 V scales multiply in (less than 2; where one multiplies in 2^n or more,
+// its 64 keys are left alone up to n less).
 template <bool INT8>
 constexpr float kTopTile = INT8 ? 14.0f : 15.0f;
 
-// An exponent is one FMA of an unrounded score product, a reference rounded:
-// they differ by up to half of fp32's step there, which up to this distance from
+// fp16 pages: an exponent is one FMA of an unrounded score product, a reference
+// rounded (with INT8 pages both come from products rounded with the K scale): they differ by up to half of fp32's step there, which up to this distance from
 // zero (in powers of two; fp16 scores reach 2^36) is at most 4.  Further on a
 // row's products are taken with a power of two instead of log2(e) / sqrt(d) and
 // are exact.  There different fp32 scores lie at least 8 powers of two apart, so
@@ -80,11 +82,12 @@ struct CfgT {
   static constexpr int SLOT = BN * D * 2;              // an fp16 K or V tile
   static constexpr int NSLOT = 131072 / SLOT;          // 4 (d = 128) or 8 (d = 64)
   static constexpr int STAGES = NSLOT / 2 + 1;         // of scales
+  static constexpr int STAGE = 256 + 4;                // floats of a stage
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int OFF_SLOT = 2 * Q_BYTES;
-  static constexpr int OFF_SCALE = OFF_SLOT + NSLOT * SLOT;         // INT8: [STAGES][2][128] scales
+  static constexpr int OFF_SCALE = OFF_SLOT + NSLOT * SLOT;         // INT8: [STAGES] K and V scales of 128 keys, 4 exponents
   static constexpr int OUT_COLS = INT8 ? 16 : 32;                   // of results on their way out, 32 rows of each softmax warp
-  static constexpr int OFF_OUT = OFF_SCALE + (INT8 ? STAGES * 256 * 4 : 0);
+  static constexpr int OFF_OUT = OFF_SCALE + (INT8 ? STAGES * STAGE * 4 : 0);
   static constexpr int OFF_BAR = OFF_OUT + 8 * 32 * OUT_COLS * 4;
   static constexpr int SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t IDESC_S = idesc_f16(BM, 64, false);
@@ -622,12 +625,16 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           // than the ring has key tiles, the next tile in this stage lands behind a release of key tile j + 1, whose
           // last S is issued behind P.V(2 j + 1).
           const uint32_t bits = __float_as_uint(__half2float(vs));
+          const uint32_t power = min(bits & 0x7f800000u, 0x43800000u);      // 2^8 at most
           if (v == 0) {
-            float* sc = scales + ((i / 2) % C::STAGES) * 256 + r;
-            sc[0] = __half2float(ks);
-            sc[128] = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);      // 1 <= |f| < 2; of a zero scale: 1
+            float* sc = scales + ((i / 2) % C::STAGES) * C::STAGE;
+            const uint32_t rest = bits - power + 0x3f800000u;               // V scale / power; of a zero scale: 1
+            sc[r] = __half2float(ks) * a.scale_log2;
+            sc[128 + r] = __uint_as_float(rest);
+            const int n = __reduce_max_sync(0xffffffffu, static_cast<int>(rest >> 23 & 255u) - 127);
+            if (lane == 0) sc[256 + (warp & 3)] = static_cast<float>(n);
           }
-          const __half2 by = __half2half2(__float2half(v ? __uint_as_float(bits & 0x7f800000u) : 1.f));
+          const __half2 by = __half2half2(__float2half(v ? __uint_as_float(power) : 1.f));
           auto widen = [&](uint4 c, uint32_t at, int q) {      // 16 codes to pieces 2 q and 2 q + 1 of a row
             const uint32_t x[4] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u};
             sts128(at + (((2 * q) ^ (r & 7)) << 4),
@@ -678,6 +685,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
     bool owed = false;    // tile 0: the other warpgroup's arrival for its last turn has not been met
     const int64_t total = a.T * Hq;
     const bool direct = p.slots == 1;
+    const float cs = INT8 ? 1.f : a.scale_log2;      // INT8: in the K scales
     while (next_segment(u, sg)) {
       const int nt = sg.nj[t];
       const int pr = 128 * t + r;
@@ -711,7 +719,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           for (int e = 0; e < HN; ++e) x[e] = __uint_as_float(v[e]);
         }
         if (INT8) {
-          const float* sc = scales + ((n + (c >> 1)) % C::STAGES) * 256 + HN * sl;
+          const float* sc = scales + ((n + (c >> 1)) % C::STAGES) * C::STAGE + HN * sl;
 #pragma unroll
           for (int e = 0; e < HN; e += 4) {
             const float4 k4 = *reinterpret_cast<const float4*>(sc + e);
@@ -719,7 +727,6 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
             f2unpack(f2mul(f2pack(x[e + 2], x[e + 3]), f2pack(k4.z, k4.w)), x[e + 2], x[e + 3]);
           }
         }
-        const float cs = a.scale_log2;
         const int key0 = sg.key0 + c * HN;
         const int nv = max(0, min((key0 < fold ? lim_prefix : lim_own) - key0, HN));
         if (!__all_sync(0xffffffffu, nv == HN)) {
@@ -727,12 +734,17 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           for (int e = 0; e < HN; ++e) x[e] = (e < nv) ? x[e] : -INFINITY;
         }
         // row's factor, and what its products are taken from: x * factor - less is the exponent
-        auto factor_of = [&]() { return fabsf(x_ref * cs) > kFarScore ? kFarScale<D> : cs; };
+        auto factor_of = [&]() { return INT8 ? 1.f : (fabsf(x_ref * cs) > kFarScore ? kFarScale<D> : cs); };
         float alpha = 1.f, factor = factor_of(), less = __fsub_rn(__fmul_rn(x_ref, factor), kPOffset);
         if (nv > 0) {
           const float top = nan_row_max<HN>(x);
           saw = true;
-          if (!(fmaf(top, factor, -less) <= kTopTile<INT8>)) {      // a NaN too: alpha, and with it l, is NaN from there on
+          float room = kTopTile<INT8>;
+          if (INT8) {
+            const float2 n2 = *reinterpret_cast<const float2*>(scales + ((n + (c >> 1)) % C::STAGES) * C::STAGE + 256 + 2 * sl);
+            room -= fmaxf(n2.x, n2.y);
+          }
+          if (!(fmaf(top, factor, -less) <= room)) {      // a NaN too: alpha, and with it l, is NaN from there on
             alpha = ex2_approx((x_ref - top) * cs);
             x_ref = top;
             factor = factor_of();
@@ -758,7 +770,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           }
           acc2[(e >> 1) & 3] = f2add(acc2[(e >> 1) & 3], f2pack(p0, p1));
           if (INT8) {
-            const float2 f = *reinterpret_cast<const float2*>(scales + ((n + (c >> 1)) % C::STAGES) * 256 + 128 + HN * sl + e);
+            const float2 f = *reinterpret_cast<const float2*>(scales + ((n + (c >> 1)) % C::STAGES) * C::STAGE + 128 + HN * sl + e);
             f2unpack(f2mul(f2pack(p0, p1), f2pack(f.x, f.y)), p0, p1);
           }
           pk[e >> 1] = pack_half2(p0, p1);
@@ -815,7 +827,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         __syncwarp();
       }
       const int64_t idx = static_cast<int64_t>(tok) * Hq + head;
-      if (row_ok && !direct) a.ml[sg.slot * total + idx] = make_float2(x_ref * a.scale_log2, l);
+      if (row_ok && !direct) a.ml[sg.slot * total + idx] = make_float2(x_ref * cs, l);
       const float inv = !direct ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
       if (nt > 0 || direct) {
         // OUT_COLS columns of the warp's 32 rows at a time through shared memory, so that a store instruction writes

@@ -146,3 +146,44 @@ def test_near_scores_far_from_zero_stay_weights(lens, new, prefix, d, int8):
         slack = vb.abs().amax(0) * (3 * ref.HALF)      # the weights' roundings against their sum, and the result's
         assert bool(((got[t0:t0 + n] <= vb.amax(0) + slack) & (got[t0:t0 + n] >= vb.amin(0) - slack)).all())
         t0 += n
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,new,prefix", PATHS)
+def test_int8_scales_of_every_size(lens, new, prefix, causal, d):
+    """Codes of the whole range -128 .. 127 under scales from 0 and fp16's smallest to its largest, V's values far past
+    fp16's among them (each of little weight, some hidden from most rows): results as the values say."""
+    hq, hkv, page = 4, 2, 64
+    g = base.gen(65)
+    table, shared, total = base.make_table(65, lens, page, extra=prefix)
+
+    def codes():
+        return torch.randint(-128, 128, (total, page, hkv, d), generator=g, device="cuda", dtype=torch.int8)
+
+    def scales(lo, hi):
+        return (2.0 ** (torch.rand(total, page, hkv, generator=g, device="cuda") * (hi - lo) + lo)).half()
+    k, ks, v, vs = codes(), scales(-24, -7), codes(), scales(-24, 4)
+    large = torch.rand(total, page, hkv, generator=g, device="cuda") < 1 / 16
+    large[table[:, 0].long().clamp(min=0)] = False           # where early rows see few keys
+    vs[large] = scales(9, 12)[large]
+    for b, n in enumerate(lens):                             # the last key: hidden from all rows but the last
+        at = int(table[b, (n - 1) // page]), (n - 1) % page
+        if n + prefix > 64:
+            vs[at], v[at] = 65504.0 / 8, -128
+        if n + prefix > 1000:
+            vs[at] = 65504.0
+    zero = torch.rand(total, page, hkv, generator=g, device="cuda") < 1 / 20
+    ks[zero], vs[zero.flip(0)] = 0.0, 0.0
+    kv = ops.PagedKV(k, v, ks, vs)
+    q = base.randn(g, sum(new), hq, d)
+    args = dict(prefix_pages=shared, prefix_len=prefix, cu_seqlens=base.offsets(new), max_seqlen=max(new), causal=causal)
+    got = ops.attn_shared_prefix(q, kv, table, base.i32(lens), **args)
+    base.ok()
+    want, tol = ref.attention(q, base.values(kv), table.cpu(), lens, new, [] if shared is None else shared.cpu().tolist(),
+                              prefix, causal)
+    fits = want.abs() + tol < 65504                          # others may round to an infinity
+    assert bool(fits.float().mean() > 0.9)
+    base.within(got.cpu()[fits], want[fits], tol[fits])
+    over = got.cpu().double()[~fits]
+    assert bool((over.sign() == want[~fits].sign()).all()) and bool((over.abs() > 65000 - tol[~fits]).all())
