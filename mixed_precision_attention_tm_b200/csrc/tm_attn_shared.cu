@@ -15,6 +15,7 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, bool int8,
                        int64_t prefix_len, int64_t max_kv_len) {
   SharedPlan p{};
   p.group = Hq / Hkv;
+  if (max_seqlen > T) max_seqlen = T;      // no sequence has more rows
   const int64_t own_packed = max_seqlen * p.group, pre_packed = T * p.group;
   int64_t own_units = ceil_div(max_kv_len, 128), pre_units = ceil_div(prefix_len, 128);
   p.own_tile = own_on_tiles(own_packed, own_units);

@@ -930,7 +930,7 @@ def kv_gather(kv, block_table, cu_seqlens_k, *, out):
 def shared_prefix_workspace_bytes(kv, batch, T, Hq, *, max_seqlen=None, prefix_len=0, max_kv_len):
     """Bytes of the workspace attn_shared_prefix needs for these sizes."""
     n = int(_lib().tm_attn_shared_prefix_workspace(int(T), int(Hq), kv.H, kv.d, int(batch),
-                                                   int(-(-T // batch) if max_seqlen is None else max_seqlen),
+                                                   int(-(-T // batch) if max_seqlen is None else min(max_seqlen, T)),
                                                    int(prefix_len), int(max_kv_len)))
     if n < 0:
         raise ValueError("bad sizes")
@@ -963,6 +963,8 @@ def attn_shared_prefix(q, kv, block_table, kv_lens, *, prefix_pages=None, prefix
         max_seqlen = T // batch
     elif max_seqlen is None:
         raise ValueError("max_seqlen comes with cu_seqlens")
+    else:
+        max_seqlen = min(max_seqlen, T)
     if Hq % kv.H:
         raise ValueError(f"{Hq} query heads over {kv.H} K/V heads")
     if out is None:

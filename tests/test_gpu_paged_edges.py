@@ -187,3 +187,18 @@ def test_int8_scales_of_every_size(lens, new, prefix, causal, d):
     base.within(got.cpu()[fits], want[fits], tol[fits])
     over = got.cpu().double()[~fits]
     assert bool((over.sign() == want[~fits].sign()).all()) and bool((over.abs() > 65000 - tol[~fits]).all())
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("lens,new,prefix", PATHS)
+def test_a_loose_bound_of_the_rows(lens, new, prefix, int8):
+    """max_seqlen far over every sequence, and over what 32 bits hold: the result of the batch's own bound."""
+    q, kv, table, shared, _ = base.attend(66, lens, new, prefix, 128, 64, 4, 2, int8)
+    args = dict(prefix_pages=shared, prefix_len=prefix, cu_seqlens=base.offsets(new))
+    want = ops.attn_shared_prefix(q, kv, table, base.i32(lens), max_seqlen=sum(new), **args)
+    for n in (100000, 2 ** 31 - 1, 2 ** 32 + 1):
+        assert torch.equal(ops.attn_shared_prefix(q, kv, table, base.i32(lens), max_seqlen=n, **args), want)
+    base.ok()
+    ref_out, tol = ref.attention(q, base.values(kv), table.cpu(), lens, new, [] if shared is None else shared.cpu().tolist(),
+                                 prefix)
+    base.within(want, ref_out, tol)

@@ -3,6 +3,11 @@
 import os
 import re
 
+from mixed_precision_attention_tm_b200 import build as tmbuild
+
+tmbuild.build()
+from mixed_precision_attention_tm_b200 import ops  # noqa: E402
+
 CSRC = os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "mixed_precision_attention_tm_b200", "csrc")
 
 
@@ -88,3 +93,21 @@ def test_tile_kernel_turns_over_several_segments():
     for segments in ([2], [2, 2], [4, 2, 0, 2], [0, 2, 0, 4], [2, 0, 0, 2, 2]):
         programs = [turn_program(t, segments, syncs[0], arrives[0], len(syncs) == 2) for t in (0, 1)]
         assert turn_faults(programs) == set(), segments
+
+
+class Pages:
+    """What the workspace query reads of a PagedKV."""
+    H, d = 8, 128
+
+
+def test_workspace_with_a_loose_bound_of_the_rows():
+    """No sequence has more rows than the batch: a larger max_seqlen is the same call, past 32 bits too."""
+    def size(n, batch=64, T=64, Hq=32):
+        return ops.shared_prefix_workspace_bytes(Pages, batch, T, Hq, max_seqlen=n, prefix_len=1000, max_kv_len=4096)
+    for n in (65, 8192, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 1, 2 ** 40):
+        assert size(n) == size(64)
+    wide = Pages()
+    wide.H = 1
+    for n in (3, 2 ** 31 - 1):
+        a = ops.shared_prefix_workspace_bytes(wide, 1, 2, 4096, max_seqlen=n, max_kv_len=1 << 20)
+        assert a == ops.shared_prefix_workspace_bytes(wide, 1, 2, 4096, max_seqlen=2, max_kv_len=1 << 20)
