@@ -615,14 +615,16 @@ tm_status tm_kv_gather(const tm_paged_kv* cache, const int32_t* table, int64_t t
  * fp32 scores, statistics and sums; P rounded to fp16 for the P.V product, the
  * one rounding besides the result's (INT8 scales are applied in fp32).  A
  * row that sees nothing is 0, one whose query holds a NaN or an infinity else
- * NaN; rows behind the last sequence are left as they were.  Values at visible
- * and causally hidden positions below kv_lens[b] must be finite; the rest of a
- * page is never used.
+ * NaN; rows before the first sequence and behind the last are left as they
+ * were.  Values at visible and causally hidden positions below kv_lens[b] must
+ * be finite; the rest of a page is never used.
  *   q, out: fp16 [T, Hq, d], Hq a multiple of the cache's H; out may be q.
  *   prefix_len = 0: plain paged attention (prefix_pages may be NULL).
- *   max_seqlen: bound on n_b (ignored without cu_seqlens); max_kv_len: bound
- *   on kv_lens[b], at most table_cols * page_size, sizes the launch; a longer
- *   sequence is recorded in the device error word and cut to it.
+ *   max_seqlen: bound on n_b (ignored without cu_seqlens; T where it is
+ *   larger); a sequence with more rows than the launch has room for is recorded
+ *   in the device error word, its result unspecified.  max_kv_len: bound on
+ *   kv_lens[b], at most table_cols * page_size, sizes the launch; a longer
+ *   sequence (with rows) is recorded in the device error word and cut to it.
  *   workspace: tm_attn_shared_prefix_workspace(...) bytes for the same
  *   arguments, 256-byte aligned, owned by the caller, overwritten; calls that
  *   may overlap on the GPU (other streams, graphs replayed side by side) need

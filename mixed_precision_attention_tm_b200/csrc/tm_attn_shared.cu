@@ -16,8 +16,10 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, bool int8,
   SharedPlan p{};
   p.group = Hq / Hkv;
   if (max_seqlen > T) max_seqlen = T;      // no sequence has more rows
+  if (max_seqlen < 1) max_seqlen = 1;      // of 0: sequences that have rows all the same are to be met
   const int64_t own_packed = max_seqlen * p.group, pre_packed = T * p.group;
   int64_t own_units = ceil_div(max_kv_len, 128), pre_units = ceil_div(prefix_len, 128);
+  if (own_units == 0 && pre_units == 0) own_units = 1;      // nothing to see: one kernel, for the zeros
   p.own_tile = own_on_tiles(own_packed, own_units);
   if (p.own_tile && prefix_len + max_kv_len < (1 << 30) &&
       prefix_folded(batch * ceil_div(own_packed, 256) * Hkv, ceil_div(pre_packed, 256) * Hkv, pre_units)) {
@@ -270,7 +272,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
   if (!prefix) {
     int64_t start64, n64;
     seq_rows(a, b, start64, n64);
-    const bool outside = start64 < 0 || n64 < 0 || start64 + n64 > a.T || n64 * g > static_cast<int64_t>(p.own_rows) * BR;
+    const bool outside = rows_outside(a, start64, n64, BR);
     if (outside && threadIdx.x == 0) dev_error(err, TM_DEVERR_SEQLEN);   // offsets that the launch was not sized for
     const int n = static_cast<int>(n64);
     if (outside || row0 >= n * g) return;
@@ -302,7 +304,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
     } else {
       for (int i = threadIdx.x; i < rows * (D / 8); i += kWarps * 32) {
         const int r = i / (D / 8);
-        if (token_of(r) < rows_in_use(a))
+        if (token_of(r) < rows_in_use(a) && token_of(r) >= first_row(a))
           *reinterpret_cast<uint4*>(a.out + token_of(r) * a.o_t + head_of(r) * a.o_h + (i % (D / 8)) * 8) =
               make_uint4(0, 0, 0, 0);
       }
@@ -709,7 +711,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
       acc[n][3] += wgt[1][w] * f.w;
     }
   }
-  const int64_t used = direct ? rows_in_use(a) : 0;
+  const int64_t used = direct ? rows_in_use(a) : 0, unused = direct ? first_row(a) : 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int r = row_of(h);
@@ -717,7 +719,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
     const int64_t t = token_of(r);
     const int64_t idx = slot * total + t * Hq + head_of(r);
     if (!direct && warp == 0 && writer) a.ml[idx] = make_float2(M[h], L[h]);
-    if (direct && t >= used) continue;
+    if (direct && (t >= used || t < unused)) continue;
     __half* oh = direct ? a.out + t * a.o_t + head_of(r) * a.o_h : nullptr;
     float* of = direct ? nullptr : a.o + idx * D;
     if (NARROW && INT8) {
@@ -798,7 +800,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const __grid_constant__ 
   const int row = static_cast<int>(blockIdx.x) * 32 + (threadIdx.x >> 3);
   const int lane = threadIdx.x & 7;
   const int t = row / Hq, h = row - t * Hq;
-  const bool live_row = row < total && t < rows_in_use(a) && (a.cu == nullptr || t >= __ldg(a.cu));
+  const bool live_row = row < total && t < rows_in_use(a) && t >= first_row(a);
   const int pre = prefix_results(p, t, h);
   const int count = live_row ? pre + p.own_splits : 0;
   const int own_at = p.pre_splits - pre;      // result i lies in slot i, or i + own_at from `pre` on
@@ -877,7 +879,7 @@ __global__ void __launch_bounds__(256, 4) join_kernel(const __grid_constant__ Sh
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (8 / W) + warp / W;
   const int part = warp % W;
   const int t = static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(Hq));     // rows stay below 2^30
-  const bool live_row = row < total && t < rows_in_use(a) && (a.cu == nullptr || t >= __ldg(a.cu));
+  const bool live_row = row < total && t < rows_in_use(a) && t >= first_row(a);
   const SharedPlan& p = a.plan;
   const int pre = prefix_results(p, t, static_cast<int>(row) - t * Hq);
   const int count = live_row ? pre + p.own_splits : 0;
@@ -955,6 +957,20 @@ __global__ void __launch_bounds__(256, 4) join_kernel(const __grid_constant__ Sh
     *reinterpret_cast<uint32_t*>(dst) = pack_half2(acc[0] * inv, acc[1] * inv);
 }
 
+// Without room for own tokens (max_kv = 0) only the prefix's kernel runs; this one makes the tests that theirs would.
+__global__ void __launch_bounds__(256) check_kernel(const __grid_constant__ SharedArgs a, DevErr err) {
+  const int64_t b = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (b < a.batch) {
+    int64_t start, n;
+    seq_rows(a, static_cast<int>(b), start, n);
+    if (rows_outside(a, start, n, a.plan.own_tile ? 256 : split_block(a.plan.narrow)) ||
+        (n > 0 && __ldg(a.kv_lens + b) > a.max_kv))
+      dev_error(err, TM_DEVERR_SEQLEN);
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+}
+
 template <int D, bool INT8, bool NARROW>
 tm_status launch_split(const SharedArgs& a, bool overlap, DevErr err, cudaStream_t stream) {
   constexpr int smem = SplitSmem<D, INT8>::BYTES;
@@ -969,12 +985,16 @@ tm_status launch_split(const SharedArgs& a, bool overlap, DevErr err, cudaStream
 }
 
 // Up to three kernels, each allowed to start while the one before it drains:
-// none of the first two reads what the other writes, the join waits for both.
+// none but the join reads what another writes, and the join waits for all.
 tm_status launch(const SharedArgs& a, int d, bool int8, DevErr err, cudaStream_t stream) {
   const SharedPlan& p = a.plan;
   bool after = false;
   tm_status st = TM_OK;
-  if (p.pre_tile) {
+  if (p.own_splits == 0) {
+    st = launch_kernel(check_kernel, ceil_div(a.batch, 256), 256, 0, after, stream, a, err);
+    after = true;
+  }
+  if (st == TM_OK && p.pre_tile) {
     st = shared_tile(a, d, int8, true, after, err, stream);
     after = true;
   }

@@ -107,6 +107,12 @@ __device__ __forceinline__ int64_t rows_in_use(const SharedArgs& a) {
   const int64_t n = a.cu != nullptr ? static_cast<int64_t>(__ldg(a.cu + a.batch)) : a.T;
   return n < a.T ? n : a.T;
 }
+__device__ __forceinline__ int64_t first_row(const SharedArgs& a) { return a.cu != nullptr ? __ldg(a.cu) : 0; }
+
+// Whether a sequence has rows that the launch was not sized for.
+__device__ __forceinline__ bool rows_outside(const SharedArgs& a, int64_t start, int64_t n, int block) {
+  return start < 0 || n < 0 || start + n > a.T || n * a.plan.group > static_cast<int64_t>(a.plan.own_rows) * block;
+}
 
 // A kernel may be launched while the one before it in the stream still runs
 // (after that one's pdl_launch_dependents); pdl_wait returns when that one has

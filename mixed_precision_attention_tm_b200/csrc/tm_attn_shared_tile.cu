@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
     s.rows = 0;
     int64_t start, n64;
     seq_rows(a, s.b, start, n64);
-    const bool outside = start < 0 || n64 < 0 || start + n64 > a.T || n64 * g > static_cast<int64_t>(p.own_rows) * 256;
+    const bool outside = rows_outside(a, start, n64, 256);
     if (outside && threadIdx.x == 0) dev_error(err, TM_DEVERR_SEQLEN);
     const int n = static_cast<int>(n64);
     if (outside || s.row0 >= n * g) return true;
@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         auto place = [&](int row, int e) {
           return stage + row * (PR * 16) + ((PR == 8 ? e ^ (row & 7) : e ^ ((row >> 1) & 3)) << 4);
         };
-        const int64_t mine = row_ok ? (direct ? tok * a.o_t + head * a.o_h : (sg.slot * total + idx) * D) : -1;
+        const int64_t mine = row_ok && !(prefix && direct && tok < first_row(a)) ? (direct ? tok * a.o_t + head * a.o_h : (sg.slot * total + idx) * D) : -1;
         int64_t at[PR];       // where rows lane / PR + RPI i go
 #pragma unroll
         for (int i = 0; i < PR; ++i) at[i] = __shfl_sync(0xffffffffu, mine, RPI * i + lane / PR);

@@ -202,3 +202,74 @@ def test_a_loose_bound_of_the_rows(lens, new, prefix, int8):
     ref_out, tol = ref.attention(q, base.values(kv), table.cpu(), lens, new, [] if shared is None else shared.cpu().tolist(),
                                  prefix)
     base.within(want, ref_out, tol)
+
+
+def reported():
+    torch.cuda.synchronize()
+    return ops.get_device_error() == ops.TM_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("lens,new,prefix", PATHS)
+def test_lengths_over_the_bound_are_reported_and_cut(lens, new, prefix, int8):
+    """kv_lens above max_kv_len: recorded, and the sequence ends at the bound."""
+    page, bound = 64, 64
+    g = base.gen(67)
+    table, shared, total = base.make_table(67, lens, page, extra=prefix)
+    kv = base.make_pool(g, total, page, 2, 128, int8)
+    q = base.randn(g, sum(new), 4, 128)
+    args = dict(prefix_pages=shared, prefix_len=prefix, cu_seqlens=base.offsets(new), max_seqlen=max(new), max_kv_len=bound)
+    cut = [min(n, bound) for n in lens]
+    want = ops.attn_shared_prefix(q, kv, table, base.i32(cut), **args)
+    base.ok()
+    got = ops.attn_shared_prefix(q, kv, table, base.i32(lens), **args)
+    assert reported() == (cut != lens)
+    assert torch.equal(got, want)
+    pages = [] if shared is None else shared.cpu().tolist()
+    ref_out, tol = ref.attention(q, base.values(kv), table.cpu(), cut, new, pages, prefix)
+    base.within(want, ref_out, tol)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("rows,prefix", [(1, 0), (1, 100), (90, 0), (90, 100), (90, 3000), (3, 6000)])
+def test_bounds_of_zero(rows, prefix, int8):
+    """max_kv_len = 0: own tokens there are all the same are recorded, the prefix alone is seen, rows before the first
+    sequence and behind the last are left.  max_seqlen = 0 with rows: right results, or an error is recorded."""
+    g = base.gen(68)
+    table, shared, total = base.make_table(68, [100, 100], 32, extra=prefix)
+    kv = base.make_pool(g, total, 32, 2, 128, int8)
+    T = 2 * rows
+    q = base.randn(g, T + 5, 8, 128)
+    cu = base.i32([2, 2 + rows, 2 + T])
+    args = dict(prefix_pages=shared, prefix_len=prefix, cu_seqlens=cu)
+    pages = [] if shared is None else shared.cpu().tolist()
+    want, tol = ref.attention(q[2:2 + T], base.values(kv), table.cpu(), [0, 0], [rows, rows], pages, prefix)
+    for lens in ([0, 0], [0, 3]):
+        out = torch.full_like(q, 5.0)
+        ops.attn_shared_prefix(q, kv, table, base.i32(lens), max_seqlen=rows, max_kv_len=0, out=out, **args)
+        assert reported() == (lens != [0, 0])
+        base.within(out[2:2 + T], want, tol)
+        assert bool((out[:2] == 5.0).all()) and bool((out[2 + T:] == 5.0).all())
+    out = torch.full_like(q, 5.0)
+    ops.attn_shared_prefix(q, kv, table, base.i32([100, 100]), max_seqlen=0, out=out, **args)
+    if not reported():
+        want, tol = ref.attention(q[2:2 + T], base.values(kv), table.cpu(), [100, 100], [rows, rows], pages, prefix)
+        base.within(out[2:2 + T], want, tol)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("prefix", [0, 300, 3000])
+def test_rows_over_their_bound_are_reported(prefix, int8):
+    """A sequence longer than the rows that max_seqlen made room for: recorded; the other sequences are what they were."""
+    g = base.gen(69)
+    new, lens = [1, 40, 2, 1], [30, 100, 90, 300]
+    table, shared, total = base.make_table(69, lens, 32, extra=prefix)
+    kv = base.make_pool(g, total, 32, 2, 128, int8)
+    q = base.randn(g, sum(new), 8, 128)
+    args = dict(prefix_pages=shared, prefix_len=prefix, cu_seqlens=base.offsets(new))
+    got = ops.attn_shared_prefix(q, kv, table, base.i32(lens), max_seqlen=2, **args).cpu()
+    assert reported()
+    pages = [] if shared is None else shared.cpu().tolist()
+    want, tol = ref.attention(q, base.values(kv), table.cpu(), lens, new, pages, prefix)
+    for rows in (slice(0, 1), slice(41, 44)):
+        base.within(got[rows], want[rows], tol[rows])
