@@ -50,6 +50,7 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, bool int8,
   const bool many = own_blocks * own_units > 13 * kSmsB200;
   if (many) chunk = ceil_div(own_blocks * own_units + pre_blocks * pre_units, 5 * kSmsB200);
   const int64_t longest = own_units > pre_units ? own_units : pre_units;
+  if (chunk > longest) chunk = longest;      // below 2^23 key tiles
   for (int64_t c = 1; !many && c <= 64 && (c == 1 || c <= longest); ++c) {
     const int64_t pre_ctas = pre_blocks * ceil_div(pre_units, c);
     const int64_t own_ctas = own_blocks * ceil_div((own_units * 6 + 9) / 10, c);

@@ -273,3 +273,25 @@ def test_rows_over_their_bound_are_reported(prefix, int8):
     want, tol = ref.attention(q, base.values(kv), table.cpu(), lens, new, pages, prefix)
     for rows in (slice(0, 1), slice(41, 44)):
         base.within(got[rows], want[rows], tol[rows])
+
+
+def test_pieces_of_a_huge_capacity():
+    """Very many sequences with room for millions of tokens each (one shared table row serves them here): a piece of the
+    own tokens is no longer than the room, and stays within 32 bits."""
+    batch, hkv, d, page = 65536, 8, 64, 256
+    cols = 13000
+    g = base.gen(70)
+    kv = base.make_pool(g, 4, page, hkv, d, False)
+    row = torch.zeros(1, cols, dtype=torch.int32, device="cuda")
+    row[0, :2] = base.i32([2, 1])
+    table = row.expand(batch, cols)
+    lens = torch.randint(1, 400, (batch,), generator=g, device="cuda", dtype=torch.int32)
+    q = base.randn(g, batch, hkv, d)
+    want = ops.attn_shared_prefix(q, kv, table, lens, max_kv_len=512)
+    got = ops.attn_shared_prefix(q, kv, table, lens)
+    base.ok()
+    pick = [0, 1, 777, batch - 1]
+    ref_out, tol = ref.attention(q[pick], base.values(kv), row.cpu().expand(4, cols), lens[pick].tolist(), [1] * 4)
+    base.within(want[pick], ref_out, tol)
+    base.within(got[pick], ref_out, tol)
+    assert float((got - want).abs().max()) <= 2.0 ** -6      # each off by its weights' rounding and its own, |v| below 8
