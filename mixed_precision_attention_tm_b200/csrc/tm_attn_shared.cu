@@ -18,6 +18,12 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, bool int8,
   if (max_seqlen > T) max_seqlen = T;      // no sequence has more rows
   if (max_seqlen < 1) max_seqlen = 1;      // of 0: sequences that have rows all the same are to be met
   const int64_t own_packed = max_seqlen * p.group, pre_packed = T * p.group;
+  // Items are counted in 32 bits, on the tile kernel by blocks that step over one another.
+  const int64_t most = 0x7fffffff - kSmsB200;
+  if (ceil_div(own_packed, 256) * batch * Hkv > most) {
+    p.bytes = -1;
+    return p;
+  }
   int64_t own_units = ceil_div(max_kv_len, 128), pre_units = ceil_div(prefix_len, 128);
   if (own_units == 0 && pre_units == 0) own_units = 1;      // nothing to see: one kernel, for the zeros
   p.own_tile = own_on_tiles(own_packed, own_units);
@@ -118,6 +124,11 @@ SharedPlan shared_plan(int64_t T, int32_t Hq, int32_t Hkv, int32_t d, bool int8,
   p.own_chunk = static_cast<int>(c * 128);
   p.own_splits = static_cast<int>(ceil_div(own_units, c));
   p.slots = p.own_splits + p.pre_splits;
+  const int64_t items = own_rows * batch * Hkv * p.own_splits + (p.pre_tile ? 0 : pre_rows * Hkv * p.pre_splits);
+  if (items > most) {
+    p.bytes = -1;
+    return p;
+  }
   const int64_t rows = T * Hq;
   p.ml_bytes = (p.slots * rows * 8 + 255) / 256 * 256;
   p.bytes = p.slots > 1 ? p.ml_bytes + p.slots * rows * d * 4 : 0;

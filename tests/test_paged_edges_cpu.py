@@ -3,6 +3,8 @@
 import os
 import re
 
+import pytest
+
 from mixed_precision_attention_tm_b200 import build as tmbuild
 
 tmbuild.build()
@@ -111,3 +113,17 @@ def test_workspace_with_a_loose_bound_of_the_rows():
     for n in (3, 2 ** 31 - 1):
         a = ops.shared_prefix_workspace_bytes(wide, 1, 2, 4096, max_seqlen=n, max_kv_len=1 << 20)
         assert a == ops.shared_prefix_workspace_bytes(wide, 1, 2, 4096, max_seqlen=2, max_kv_len=1 << 20)
+
+
+def test_launches_whose_items_pass_32_bits_are_refused():
+    """A block of the tile kernel goes from item to item in steps of the grid: the last step stays below 2^31 too."""
+    few = Pages()
+    few.H = 63
+    for batch, fits in ((34087042, False), (34087040, False), (34000000, True)):       # 63 items each: 2^31 - 2, 2^31 - 128
+        def size():
+            return ops.shared_prefix_workspace_bytes(few, batch, 100, 63, max_seqlen=100, max_kv_len=64)
+        if fits:
+            assert size() > 0
+        else:
+            with pytest.raises(ValueError):
+                size()
