@@ -866,8 +866,9 @@ def block_table_check(block_table, kv_lens, num_pages, page_size):
     does not hold kv_lens[b] tokens of each sequence in pages 0 ..
     num_pages - 1 (tm_block_table_check): the test that the kernels make of
     each page, before anything is launched."""
-    t = torch.as_tensor(block_table, dtype=torch.int32, device="cpu").contiguous()
-    n = torch.as_tensor(kv_lens, dtype=torch.int32, device="cpu").contiguous()
+    # to 32 bits: what lies outside is no page, and longer than any table
+    t, n = (torch.as_tensor(x, dtype=torch.int64, device="cpu").clamp(-1, 2 ** 31 - 1).to(torch.int32).contiguous()
+            for x in (block_table, kv_lens))
     if t.dim() != 2 or n.dim() != 1 or n.shape[0] > t.shape[0]:
         raise ValueError("block_table [batch, columns] and kv_lens [batch] expected")
     bad = (ctypes.c_int32 * 2)(-1, -1)

@@ -4,6 +4,7 @@ import os
 import re
 
 import pytest
+import torch
 
 from mixed_precision_attention_tm_b200 import build as tmbuild
 
@@ -127,3 +128,19 @@ def test_launches_whose_items_pass_32_bits_are_refused():
         else:
             with pytest.raises(ValueError):
                 size()
+
+
+def test_block_table_check_of_64_bit_tables():
+    """Page numbers and lengths past 32 bits are what they are, not what is left of them."""
+    ops.block_table_check(torch.tensor([[3, 1]]), torch.tensor([32]), 4, 16)
+    for page in (2 ** 32 + 1, 2 ** 32, -2 ** 32 + 3, 2 ** 31, -1, 2 ** 63 - 1):
+        with pytest.raises(ValueError, match="sequence 0, column 1"):
+            ops.block_table_check(torch.tensor([[3, page]]), torch.tensor([32]), 4, 16)
+        with pytest.raises(ValueError, match="sequence 0, column 1"):
+            ops.block_table_check([[3, page]], [32], 4, 16)
+        ops.block_table_check(torch.tensor([[3, page]]), torch.tensor([16]), 4, 16)
+    for n in (33, 2 ** 31, 2 ** 32, 2 ** 32 + 16, 2 ** 63 - 1):
+        with pytest.raises(ValueError, match="sequence 0, column 2"):
+            ops.block_table_check(torch.tensor([[3, 1]]), torch.tensor([n]), 4, 16)
+    ops.block_table_check(torch.tensor([[3, 1]]), torch.tensor([-2 ** 32 + 33]), 4, 16)      # empty
+    ops.block_table_check(torch.tensor([[3, 1]]), [], 4, 16)
