@@ -143,4 +143,3 @@ def test_block_table_check_of_64_bit_tables():
         with pytest.raises(ValueError, match="sequence 0, column 2"):
             ops.block_table_check(torch.tensor([[3, 1]]), torch.tensor([n]), 4, 16)
     ops.block_table_check(torch.tensor([[3, 1]]), torch.tensor([-2 ** 32 + 33]), 4, 16)      # empty
-    ops.block_table_check(torch.tensor([[3, 1]]), [], 4, 16)
