@@ -577,12 +577,13 @@ tm_status tm_block_table_check(const int32_t* table_host, int64_t table_stride, 
  * (device int32) is the length of sequence b AFTER the append: its new row i
  * of n goes to own position j = kv_lens[b] - n + i and is rotated at position
  * j + pos_offset (pos_offset: the length of a shared prefix).  Rows with j < 0
- * (padding) and rows behind the last sequence are not appended.
+ * (padding), and rows before the first sequence and behind the last, are not
+ * appended.
  *   k_weight / q_weight: fp16 [d] norm weights or NULL (no norm), eps as above;
  *   rope: NULL for no rotation;
  *   q, q_out: NULL, or the same tokens' queries, normed with q_weight and
- *   rotated into q_out in the same launch (rows behind the last sequence are
- *   left as they were).
+ *   rotated into q_out in the same launch (rows before the first sequence and
+ *   behind the last are left as they were).
  * K is computed in fp32 and rounded once (fp16 pages) or quantised from fp32
  * (INT8 pages); INT8: scale = fp16(amax / 127), code = clamp(rne(x / scale),
  * -127, 127), all codes 0 where the scale is 0 (a row that holds a NaN or an
@@ -597,8 +598,8 @@ tm_status tm_kv_append(const tm_tensor* k, const tm_tensor* v, const tm_paged_kv
  * tm_kv_gather -- cached rows back into contiguous fp16 tensors, as the
  * prefill attention over separate key offsets reads them: row
  * cu_seqlens_k[b] + j of k_out / v_out [T, H, d] is own position j of sequence
- * b (INT8 pages: fp16(code * scale)).  Rows behind the last sequence, and rows
- * whose page number is bad, are left as they were. */
+ * b (INT8 pages: fp16(code * scale)).  Rows before the first sequence and behind
+ * the last, and rows whose page number is bad, are left as they were. */
 tm_status tm_kv_gather(const tm_paged_kv* cache, const int32_t* table, int64_t table_stride, int32_t table_cols,
                        const int32_t* cu_seqlens_k, int32_t batch, tm_tensor* k_out, tm_tensor* v_out, void* stream);
 

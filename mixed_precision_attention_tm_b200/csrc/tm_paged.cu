@@ -106,8 +106,8 @@ kv_gather_kernel(PagedPool pool, PageTable pt, const int32_t* __restrict__ cu, i
     if (t < T && (R == 1 || lane < R)) {
       if (R > 1)
         while (b < batch && __ldg(cu + b + 1) <= t) ++b;
-      if (b < batch) {
-        const int64_t j = t - __ldg(cu + b);
+      const int64_t j = b < batch ? t - __ldg(cu + b) : -1;      // negative before the first sequence, too
+      if (j >= 0) {
         const int32_t page = page_of(pt, b, j);
         if (page < 0) {
           if (R > 1 || lane == 0) dev_error(err, TM_DEVERR_SEQLEN);

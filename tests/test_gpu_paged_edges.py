@@ -295,3 +295,21 @@ def test_pieces_of_a_huge_capacity():
     base.within(want[pick], ref_out, tol)
     base.within(got[pick], ref_out, tol)
     assert float((got - want).abs().max()) <= 2.0 ** -6      # each off by its weights' rounding and its own, |v| below 8
+
+
+@pytest.mark.parametrize("d,page,hq,hkv,int8,order", base.CACHES)
+@pytest.mark.parametrize("lens", [[9, 33, 0, 700, 16], [5] * 70, [40000, 20, 2000]])
+def test_gather_of_the_last_sequences_of_a_batch(d, page, hq, hkv, int8, order, lens):
+    """Offsets that begin behind row 0 (the rest of a longer batch): rows before them are left as they were, and are no
+    error."""
+    g = base.gen(71 + sum(lens))
+    table, _, total = base.make_table(71, lens, page)
+    kv = base.make_pool(g, total, page, hkv, d, int8, order)
+    T, cu = sum(lens), base.offsets(lens)
+    whole, rest = (tuple(torch.full((T + 3, hkv, d), 5.0, dtype=torch.float16, device="cuda") for _ in range(2)) for _ in range(2))
+    ops.kv_gather(kv, table, cu, out=whole)
+    base.ok()
+    ops.kv_gather(kv, table[1:], cu[1:], out=rest)
+    base.ok()
+    for a, b in zip(whole, rest):
+        assert torch.equal(a[lens[0]:], b[lens[0]:]) and bool((b[:lens[0]] == 5.0).all())
