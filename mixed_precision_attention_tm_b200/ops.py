@@ -930,6 +930,8 @@ def kv_gather(kv, block_table, cu_seqlens_k, *, out):
 
 def shared_prefix_workspace_bytes(kv, batch, T, Hq, *, max_seqlen=None, prefix_len=0, max_kv_len):
     """Bytes of the workspace attn_shared_prefix needs for these sizes."""
+    if batch < 1:
+        raise ValueError("at least one sequence expected")
     n = int(_lib().tm_attn_shared_prefix_workspace(int(T), int(Hq), kv.H, kv.d, int(batch),
                                                    int(-(-T // batch) if max_seqlen is None else min(max_seqlen, T)),
                                                    int(prefix_len), int(max_kv_len)))

@@ -143,3 +143,10 @@ def test_block_table_check_of_64_bit_tables():
         with pytest.raises(ValueError, match="sequence 0, column 2"):
             ops.block_table_check(torch.tensor([[3, 1]]), torch.tensor([n]), 4, 16)
     ops.block_table_check(torch.tensor([[3, 1]]), torch.tensor([-2 ** 32 + 33]), 4, 16)      # empty
+
+
+def test_workspace_of_no_sequences_is_refused():
+    for batch in (0, -1):
+        for n in (None, 4):
+            with pytest.raises(ValueError):
+                ops.shared_prefix_workspace_bytes(Pages, batch, 8, 32, max_seqlen=n, max_kv_len=64)
