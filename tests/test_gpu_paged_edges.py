@@ -313,3 +313,48 @@ def test_gather_of_the_last_sequences_of_a_batch(d, page, hq, hkv, int8, order, 
     base.ok()
     for a, b in zip(whole, rest):
         assert torch.equal(a[lens[0]:], b[lens[0]:]) and bool((b[:lens[0]] == 5.0).all())
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,new,prefix", PATHS)
+def test_infinities_where_nothing_is_read(lens, new, prefix, causal, int8):
+    """Infinities and NaN in the slots behind a sequence's end, behind the prefix's, and in pages of no sequence."""
+    page = 64
+    g = base.gen(72)
+    table, shared, total = base.make_table(72, lens, page, extra=prefix)
+    kv = base.make_pool(g, total, page, 2, 128, int8)
+    q = base.randn(g, sum(new), 4, 128)
+    args = dict(prefix_pages=shared, prefix_len=prefix, cu_seqlens=base.offsets(new), max_seqlen=max(new), causal=causal)
+    want = ops.attn_shared_prefix(q, kv, table, base.i32(lens), **args)
+    unused = torch.ones(total, page, dtype=torch.bool)
+    for pages, n in [([] if shared is None else shared.tolist(), prefix)] + [(table[b].tolist(), n) for b, n in enumerate(lens)]:
+        for i, p in enumerate(pages[:-(-n // page)]):
+            unused[p, :max(0, min(page, n - i * page))] = False
+    at = unused.cuda().nonzero()
+    junk = torch.tensor([float("inf"), float("-inf"), float("nan")], dtype=torch.float16, device="cuda")
+    for x in (kv.k_scales, kv.v_scales) if int8 else (kv.k, kv.v):
+        fill = junk[torch.arange(len(at), device="cuda") % 3]
+        x[at[:, 0], at[:, 1]] = fill.view(-1, *[1] * (x.dim() - 2)).expand(-1, *x.shape[2:])
+    got = ops.attn_shared_prefix(q, kv, table, base.i32(lens), **args)
+    base.ok()
+    assert torch.equal(got, want) and bool(want.isfinite().all())
+
+
+@pytest.mark.parametrize("d,int8", [(128, False), (128, True), (64, False), (64, True)])
+@pytest.mark.parametrize("lens,new,prefix", PATHS + [([300, 5, 1000, 64], [1, 1, 1, 1], 0), ([1] * 9, [1] * 9, 100)])
+def test_a_capacity_far_over_the_lengths(lens, new, prefix, d, int8):
+    """max_kv_len at a table's capacity of 32768 tokens: the results of the lengths, and none past a short table row."""
+    page = 64
+    g = base.gen(73)
+    table, shared, total = base.make_table(73, lens, page, extra=prefix)
+    kv = base.make_pool(g, total, page, 2, d, int8)
+    q = base.randn(g, sum(new), 8, d, scale=2.0)
+    wide = torch.full((len(lens), 512), -7, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    got = ops.attn_shared_prefix(q, kv, wide, base.i32(lens), prefix_pages=shared, prefix_len=prefix,
+                                 cu_seqlens=base.offsets(new), max_seqlen=max(new))
+    base.ok()
+    want, tol = ref.attention(q, base.values(kv), table.cpu(), lens, new, [] if shared is None else shared.cpu().tolist(),
+                              prefix)
+    base.within(got, want, tol)
