@@ -576,7 +576,7 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
       for (int h = 0; h < 2; ++h) {
         for (int w = NARROW ? 4 : 1; w < (NARROW ? 32 : 4); w *= 2) mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], w));
         const float mn = fmaxf(m[h], mx[h]);
-        scale[h] = ex2_approx(m[h] - (mn == -INFINITY ? 0.f : mn));
+        scale[h] = ex2_approx((m[h] - kPOffset) - (mn == -INFINITY ? 0.f : mn - kPOffset));      // as the exponents take them
         m[h] = mn;
         l[h] *= scale[h];
       }
@@ -678,8 +678,8 @@ __device__ __forceinline__ void split_rows(const SharedArgs& a, const PageMaps& 
   // ---- join the four warps, in fragment order: register e of n-tile n of lane
   const bool writer = NARROW ? r8 == 0 : quad == 0;      // of its rows' m and l
   if (writer) {
-    ml_s[warp * 16 + row_of(0)] = make_float2(m[0], l[0]);
-    ml_s[warp * 16 + row_of(1)] = make_float2(m[1], l[1]);
+    ml_s[warp * 16 + row_of(0)] = make_float2(m[0] - kPOffset, l[0]);
+    ml_s[warp * 16 + row_of(1)] = make_float2(m[1] - kPOffset, l[1]);
   }
   __syncwarp();
   static_assert(NT * 32 * 16 <= kStages * 2 * S::BYTES, "a warp's O fits its ring");

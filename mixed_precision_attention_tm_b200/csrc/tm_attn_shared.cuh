@@ -6,8 +6,8 @@
 // query head kv_head * g + r % g, g = Hq / Hkv, so that every byte of K and V
 // is used for all rows that see it.  Keys are cut into ranges ("splits"); a
 // split's result for a row is (O, m, l): a reference m of its scores in powers
-// of two (a maximum of some time), l = sum 2^(s - m + kPOffset) and O = the same sum of
-// weighted values, fp32.  One slot of the workspace holds one split's results
+// of two (a maximum of some time, less kPOffset), l = sum 2^(s - m) and O = the same sum
+// of weighted values, fp32.  One slot of the workspace holds one split's results
 // of all rows, prefix splits first; results join as
 //   out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,  M = max m_i.
 #pragma once

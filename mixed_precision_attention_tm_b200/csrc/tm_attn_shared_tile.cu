@@ -47,25 +47,19 @@
 namespace tmk {
 namespace {
 
-// 2^kPOffset is the largest weight when the reference is the maximum; scores
-// above it are left alone up to this exponent: 2^15 at most, inside fp16, with
-// what INT8 V scales multiply in (less than 2; where one multiplies in 2^n or more,
-// its 64 keys are left alone up to n less).
+// 2^kPOffset is the largest weight when the reference is the maximum (far from zero
+// 1); scores above it are left alone up to this exponent: 2^15 at most, inside fp16, with
+// what INT8 V scales multiply in (less than 2; where one of 64 keys multiplies in
+// up to 256, these are left alone up to 7 less).
 template <bool INT8>
 constexpr float kTopTile = INT8 ? 14.0f : 15.0f;
 
 // fp16 pages: an exponent is one FMA of an unrounded score product, a reference
-// rounded (with INT8 pages both come from products rounded with the K scale): they differ by up to half of fp32's step there, which up to this distance from
-// zero (in powers of two; fp16 scores reach 2^36) is at most 4.  Further on a
-// row's products are taken with a power of two instead of log2(e) / sqrt(d) and
-// are exact.  There different fp32 scores lie at least 8 powers of two apart, so
-// that what such a row loses is a lesser weight's size: 2^-8 may count as 2^-8.2
-// (d = 128), 2^-11.5 as 2^-16 (d = 64).  Rounding each product for these rows instead
-// took a branch before the exponentials (16 chunks of prompts behind 16384 positions: 551 us
-// a call instead of 540 to 547).
-constexpr float kFarScore = 134217728.0f;
-template <int D>
-constexpr float kFarScale = D == 128 ? 0.125f : 0.25f;
+// rounded (with INT8 pages both come from products rounded with the K scale).  Up to
+// this distance from zero (in powers of two; fp16 scores reach 2^36) they differ
+// by an eighth at most; a row whose reference lies further out has its products
+// taken from that reference, which is exact for those that count.
+constexpr float kFarScore = 4194304.0f;
 
 // Of every 8 pairs of exponentials, how many run on the FMA pipe: the special
 // function unit alone takes as long as the MMAs of a tile.  A 64-key step of both
@@ -82,12 +76,11 @@ struct CfgT {
   static constexpr int SLOT = BN * D * 2;              // an fp16 K or V tile
   static constexpr int NSLOT = 131072 / SLOT;          // 4 (d = 128) or 8 (d = 64)
   static constexpr int STAGES = NSLOT / 2 + 1;         // of scales
-  static constexpr int STAGE = 256 + 4;                // floats of a stage
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int OFF_SLOT = 2 * Q_BYTES;
-  static constexpr int OFF_SCALE = OFF_SLOT + NSLOT * SLOT;         // INT8: [STAGES] K and V scales of 128 keys, 4 exponents
+  static constexpr int OFF_SCALE = OFF_SLOT + NSLOT * SLOT;         // INT8: [STAGES][2][128] scales
   static constexpr int OUT_COLS = INT8 ? 16 : 32;                   // of results on their way out, 32 rows of each softmax warp
-  static constexpr int OFF_OUT = OFF_SCALE + (INT8 ? STAGES * STAGE * 4 : 0);
+  static constexpr int OFF_OUT = OFF_SCALE + (INT8 ? STAGES * 256 * 4 : 0);
   static constexpr int OFF_BAR = OFF_OUT + 8 * 32 * OUT_COLS * 4;
   static constexpr int SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t IDESC_S = idesc_f16(BM, 64, false);
@@ -627,12 +620,10 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           const uint32_t bits = __float_as_uint(__half2float(vs));
           const uint32_t power = min(bits & 0x7f800000u, 0x43800000u);      // 2^8 at most
           if (v == 0) {
-            float* sc = scales + ((i / 2) % C::STAGES) * C::STAGE;
+            float* sc = scales + ((i / 2) % C::STAGES) * 256;
             const uint32_t rest = bits - power + 0x3f800000u;               // V scale / power; of a zero scale: 1
             sc[r] = __half2float(ks) * a.scale_log2;
             sc[128 + r] = __uint_as_float(rest);
-            const int n = __reduce_max_sync(0xffffffffu, static_cast<int>(rest >> 23 & 255u) - 127);
-            if (lane == 0) sc[256 + (warp & 3)] = static_cast<float>(n);
           }
           const __half2 by = __half2half2(__float2half(v ? __uint_as_float(power) : 1.f));
           auto widen = [&](uint4 c, uint32_t at, int q) {      // 16 codes to pieces 2 q and 2 q + 1 of a row
@@ -696,7 +687,9 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       const int lim_prefix = row_ok ? prefix_len : 0;
       int lim_own = fold;
       if (row_ok && !prefix) lim_own += max(0, a.causal ? min(sg.lk, sg.hidden + tok_in) : sg.lk);
-      float x_ref = -INFINITY, l = 0.f;      // reference: a score product of the row
+      // Reference (a score product of the row, counted from `base`), and the exponent of product x by it: x * cs - less.
+      // Before the first one every finite product exceeds it, and a hidden one's exponent is -inf.
+      float x_ref = -INFINITY, base = 0.f, less = -1e30f, l = 0.f;
       bool saw = false;      // a key
       // The two softmax warpgroups take turns at their exponentials: side by side they would slow each other down
       // into lockstep, and stores, waits and handoffs of both would leave the SM idle at the same time.
@@ -709,51 +702,53 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         mbar_wait(bar(T_SFULL + 2 * t + sl), (cc >> 1) & 1, err, abort_flag);
         tc_fence_after();
         __syncwarp();
-        float x[HN];
-        {
-          uint32_t v[HN];
+        float2 mine = make_float2(1.f, 1.f);      // INT8: what two of the keys' V scales multiply in
+        if (INT8) mine = *reinterpret_cast<const float2*>(scales + ((n + (c >> 1)) % C::STAGES) * 256 + 128 + HN * sl + 2 * lane);
+        float x[HN], alpha = 1.f;
+        for (;;) {
+          {
+            uint32_t v[HN];
 #pragma unroll
-          for (int q = 0; q < HN / 32; ++q) tmem_ld32p(s_c + q * 32, v + q * 32);
-          tmem_wait_ld_regs<HN>(v);
+            for (int q = 0; q < HN / 32; ++q) tmem_ld32p(s_c + q * 32, v + q * 32);
+            tmem_wait_ld_regs<HN>(v);
 #pragma unroll
-          for (int e = 0; e < HN; ++e) x[e] = __uint_as_float(v[e]);
-        }
-        if (INT8) {
-          const float* sc = scales + ((n + (c >> 1)) % C::STAGES) * C::STAGE + HN * sl;
-#pragma unroll
-          for (int e = 0; e < HN; e += 4) {
-            const float4 k4 = *reinterpret_cast<const float4*>(sc + e);
-            f2unpack(f2mul(f2pack(x[e], x[e + 1]), f2pack(k4.x, k4.y)), x[e], x[e + 1]);
-            f2unpack(f2mul(f2pack(x[e + 2], x[e + 3]), f2pack(k4.z, k4.w)), x[e + 2], x[e + 3]);
+            for (int e = 0; e < HN; ++e) x[e] = __uint_as_float(v[e]);
           }
-        }
-        const int key0 = sg.key0 + c * HN;
-        const int nv = max(0, min((key0 < fold ? lim_prefix : lim_own) - key0, HN));
-        if (!__all_sync(0xffffffffu, nv == HN)) {
-#pragma unroll
-          for (int e = 0; e < HN; ++e) x[e] = (e < nv) ? x[e] : -INFINITY;
-        }
-        // row's factor, and what its products are taken from: x * factor - less is the exponent
-        auto factor_of = [&]() { return INT8 ? 1.f : (fabsf(x_ref * cs) > kFarScore ? kFarScale<D> : cs); };
-        float alpha = 1.f, factor = factor_of(), less = __fsub_rn(__fmul_rn(x_ref, factor), kPOffset);
-        if (nv > 0) {
-          const float top = nan_row_max<HN>(x);
-          saw = true;
-          float room = kTopTile<INT8>;
           if (INT8) {
-            const float2 n2 = *reinterpret_cast<const float2*>(scales + ((n + (c >> 1)) % C::STAGES) * C::STAGE + 256 + 2 * sl);
-            room -= fmaxf(n2.x, n2.y);
+            const float* sc = scales + ((n + (c >> 1)) % C::STAGES) * 256 + HN * sl;
+#pragma unroll
+            for (int e = 0; e < HN; e += 4) {
+              const float4 k4 = *reinterpret_cast<const float4*>(sc + e);
+              f2unpack(f2mul(f2pack(x[e], x[e + 1]), f2pack(k4.x, k4.y)), x[e], x[e + 1]);
+              f2unpack(f2mul(f2pack(x[e + 2], x[e + 3]), f2pack(k4.z, k4.w)), x[e + 2], x[e + 3]);
+            }
           }
-          if (!(fmaf(top, factor, -less) <= room)) {      // a NaN too: alpha, and with it l, is NaN from there on
-            alpha = ex2_approx((x_ref - top) * cs);
-            x_ref = top;
-            factor = factor_of();
-            less = __fsub_rn(__fmul_rn(x_ref, factor), kPOffset);
+          const int key0 = sg.key0 + c * HN;
+          const int nv = max(0, min((key0 < fold ? lim_prefix : lim_own) - key0, HN));
+          if (!__all_sync(0xffffffffu, nv == HN && (INT8 || base == 0.f))) {
+#pragma unroll
+            for (int e = 0; e < HN; ++e) x[e] = (e < nv) ? (INT8 ? x[e] : x[e] - base) : -INFINITY;
           }
+          float room = kTopTile<INT8>;
+          if (INT8 && __any_sync(0xffffffffu, fmaxf(fabsf(mine.x), fabsf(mine.y)) >= 2.f)) room -= 7.f;
+          bool far = false;
+          if (nv > 0) {
+            const float top = nan_row_max<HN>(x);
+            saw = true;
+            if (!(fmaf(top, cs, -less) <= room)) {      // a NaN too: alpha, and with it l, is NaN from there on
+              far = !INT8 && fabsf(top * cs) > kFarScore;
+              if (far) base += top;
+              x_ref = far ? 0.f : top;
+              const float before = far ? fmaf(-top, cs, less) : less;
+              less = __fsub_rn(__fmul_rn(x_ref, cs), base == 0.f ? kPOffset : 0.f);      // 6 would be lost next to base * cs
+              alpha = ex2_approx(before - less);
+            }
+          }
+          // with a new base once more, from the scores in tensor memory
+          if (INT8 || !__any_sync(0xffffffffu, far)) break;
         }
         if (c < turns && (t == 1 || c > 0 || owed)) named_bar_sync(NB_TURN + t, 256);
-        if (x_ref == -INFINITY) less = 0.f;
-        const uint64_t c2 = f2pack(factor, factor), nm2 = f2pack(-less, -less);
+        const uint64_t c2 = f2pack(cs, cs), nm2 = f2pack(-less, -less);
         uint32_t pk[HN / 2];
         uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -770,7 +765,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
           }
           acc2[(e >> 1) & 3] = f2add(acc2[(e >> 1) & 3], f2pack(p0, p1));
           if (INT8) {
-            const float2 f = *reinterpret_cast<const float2*>(scales + ((n + (c >> 1)) % C::STAGES) * C::STAGE + 128 + HN * sl + e);
+            const float2 f = *reinterpret_cast<const float2*>(scales + ((n + (c >> 1)) % C::STAGES) * 256 + 128 + HN * sl + e);
             f2unpack(f2mul(f2pack(p0, p1), f2pack(f.x, f.y)), p0, p1);
           }
           pk[e >> 1] = pack_half2(p0, p1);
@@ -819,7 +814,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
       // A row that saw nothing has no weight.  Of a query that is not finite all scores are NaN or infinities: NaN, which
       // the weights alone need not show (the exponentials on the FMA pipe clamp a NaN to 2^-125).
       if (!saw) l = 0.f;
-      else if (!(fabsf(x_ref) < INFINITY)) l = NAN;
+      else if (!(fabsf(base + x_ref) < INFINITY)) l = NAN;
       if (nt > 0) {
         mbar_wait(bar(T_OLAST + t), segs & 1, err, abort_flag);
         ++segs;
@@ -827,7 +822,7 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         __syncwarp();
       }
       const int64_t idx = static_cast<int64_t>(tok) * Hq + head;
-      if (row_ok && !direct) a.ml[sg.slot * total + idx] = make_float2(x_ref * cs, l);
+      if (row_ok && !direct) a.ml[sg.slot * total + idx] = make_float2(x_ref == -INFINITY ? x_ref : base * cs + less, l);
       const float inv = !direct ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
       if (nt > 0 || direct) {
         // OUT_COLS columns of the warp's 32 rows at a time through shared memory, so that a store instruction writes

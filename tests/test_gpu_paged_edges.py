@@ -1,5 +1,7 @@
 """Paged-cache serving operators on the GPU at the edges of their contract, against their 64-bit forms."""
 
+import math
+
 import pytest
 import torch
 
@@ -358,3 +360,37 @@ def test_a_capacity_far_over_the_lengths(lens, new, prefix, d, int8):
     want, tol = ref.attention(q, base.values(kv), table.cpu(), lens, new, [] if shared is None else shared.cpu().tolist(),
                               prefix)
     base.within(got, want, tol)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("around", [2.0 ** 22, -2.0 ** 22, 2.0 ** 21, 2.0 ** 23, 2.0 ** 27])
+@pytest.mark.parametrize("rising", [True, False])
+def test_near_scores_far_from_zero_on_a_tile(around, rising, d):
+    """Scores 2^22 powers of two from zero, where a tile's references change their form, a few units apart and exact in
+    fp32: rows of one tile, whose exponents come from exact products, weigh them as 64 bits do."""
+    n, hq, hkv, page = 100, 4, 2, 64
+    g = base.gen(74)
+    table, _, total = base.make_table(74, [n, n], page)
+    kv = base.make_pool(g, total, page, hkv, d, False)
+    unit = 2.0 ** (round(math.log2(abs(around) * math.sqrt(d) * math.log(2))) - 20)      # of the sums: 16 of fp32's steps
+    big = round(around * math.sqrt(d) * math.log(2) / unit) - 10                         # about 2^20 units
+    step = torch.randint(0, 8, (total, page), generator=g, device="cuda")
+    for b in range(2):                           # later keys higher (or lower) by up to 24 units
+        for j in range(n):
+            step[int(table[b, j // page]), j % page] += (j if rising else n - j) // 4
+    scale = 2.0 ** round(math.log2(unit) / 2)    # sums of products: (hi 2^10 + lo) units, and the step
+    hi, lo = divmod(big, 1024)
+    keys = torch.zeros(total, page, d, device="cuda")
+    keys[..., 0], keys[..., 1], keys[..., 2] = hi * scale, lo * scale, step * scale
+    fill_keys(kv, keys.half())
+    q = torch.zeros(2 * n, hq, d, dtype=torch.float16, device="cuda")
+    other = unit / scale
+    q[..., 0], q[..., 1], q[..., 2] = 1024 * other, other, other
+    got = ops.attn_shared_prefix(q, kv, table, base.i32([n, n]), max_kv_len=n)
+    base.ok()
+    values = base.values(kv)
+    assert bool((values[0][..., 0] == hi * scale).all()) and bool((q[..., 0] == 1024 * other).all())
+    want, _ = ref.attention(q, values, table.cpu(), [n, n], [n, n])
+    size, _ = ref.attention(q, (values[0], values[1].abs()), table.cpu(), [n, n], [n, n])
+    # weights to 2^-17 of an exact exponent, rounded once, their sum the same; the result's rounding
+    base.within(got, want, size * (2 * ref.HALF + 2.0 ** -15) + n * 2.0 ** -24 * 8 + ref.TINY)
