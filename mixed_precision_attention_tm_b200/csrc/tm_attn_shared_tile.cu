@@ -832,7 +832,8 @@ __global__ void __launch_bounds__(CfgT<D, INT8>::THREADS, 1)
         auto place = [&](int row, int e) {
           return stage + row * (PR * 16) + ((PR == 8 ? e ^ (row & 7) : e ^ ((row >> 1) & 3)) << 4);
         };
-        const int64_t mine = row_ok && !(prefix && direct && tok < first_row(a)) ? (direct ? tok * a.o_t + head * a.o_h : (sg.slot * total + idx) * D) : -1;
+        const bool wanted = row_ok && !(prefix && direct && tok < first_row(a));
+        const int64_t mine = wanted ? (direct ? tok * a.o_t + head * a.o_h : (sg.slot * total + idx) * D) : -1;
         int64_t at[PR];       // where rows lane / PR + RPI i go
 #pragma unroll
         for (int i = 0; i < PR; ++i) at[i] = __shfl_sync(0xffffffffu, mine, RPI * i + lane / PR);
