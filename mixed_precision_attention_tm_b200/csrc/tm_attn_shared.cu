@@ -212,7 +212,8 @@ struct SplitSmem {
 // d = 128 in fp16 two CTAs (eight warps, 192 KB of rings) fit an SM, else
 // three or four.  Measured with 32 single tokens, 32 query heads over 8: behind
 // 16000 own tokens each, fp16, 2.1 GB in 299 us (7.0 TB/s, HBM's rate); INT8, 1.07
-// GB in 215 us (5.0 TB/s: the conversion's instructions); behind 200 to 2000,
+// GB in 215 us (5.0 TB/s: four warps a scheduler wait for one another's chains of
+// dependent instructions, the conversion's among them); behind 200 to 2000,
 // where starts, ends and the join weigh, 144 MB in 30 us.  A step's keys lie in one page, so a TMA copy
 // brings its K (two at d = 128 in fp16), another its V, for a dozen
 // instructions where row copies took over a hundred.  A step that the range

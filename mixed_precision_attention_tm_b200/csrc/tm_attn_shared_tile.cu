@@ -32,7 +32,7 @@
 // score products read Q from shared memory again for every 64 keys), its
 // exponentials on the special function unit alone 1024, the rest of the softmax a few hundred issue
 // slots of each warp; together 1460 to 1550 cycles, about 1.2 PFLOP/s (7200 packed
-// rows of 8 K/V heads behind 16384 positions: 405 us).  With few key tiles for a CTA
+// rows of 8 K/V heads behind 16384 positions: 400 us).  With few key tiles for a CTA
 // its start (setup, first copies, cold instructions: 5 us) and its results (128 KB)
 // count as much.
 #include <cuda_fp16.h>

@@ -11,8 +11,9 @@
 // and single steps by latency.  Rotation of 16384 tokens, 32 + 8 heads of 128
 // (336 MB): 53.5 us, 0.96 of the measured copy bandwidth.  Norm and rotation of 8191
 // tokens, 32 + 8 heads of 64 (84 MB): 16.3 us, 0.79 of it.  Appending 9616 tokens to
-// INT8 pages, 4 heads of 128 with 32 query heads rotated (187 MB): 41 us, 0.70 of it;
-// the codes' rounding and packing take issue slots.  64 tokens: 3.5 us, a chain of loads.
+// INT8 pages, 4 heads of 128 with 32 query heads rotated (187 MB): 41 us, 0.70 of it:
+// a third of the warps fit, and wait for loads first (issue slots 55 % used).  64 tokens:
+// 3.5 us, a chain of loads.
 //
 // Angles: a frequency is a 64-bit binary fraction F of a turn per position, so
 // p * F mod 2^64 is the angle as a fraction of a turn without range reduction
