@@ -63,8 +63,8 @@ constexpr float kFarScore = 4194304.0f;
 
 // Of every 8 pairs of exponentials, how many run on the FMA pipe: the special
 // function unit alone takes as long as the MMAs of a tile.  fp16, 7200 packed rows of 8
-// K/V heads behind 16384 positions: 545 us a call with 0, 510 with 2, 520 with 3, 535 with 4 (on
-// another day 510 with 1, 494 with 2, 500 with 3).  With INT8 pages the conversion
+// K/V heads behind 16384 positions: 545 us a call with 0, 510 with 2, 520 with 3, 535 with 4 (in
+// another run 510 with 1, 494 with 2, 500 with 3).  With INT8 pages the conversion
 // warps want the same pipes: 1024 tokens of 4 K/V heads behind 16384 positions 374 us
 // with 0, 379 with 1, 390 with 2.
 template <bool INT8>
